@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -20,10 +21,11 @@ BL_OK = 0
 STATUS_NAMES = {
     0: "BL_OK", 1: "BL_ERR_NULL", 2: "BL_ERR_SHAPE", 3: "BL_ERR_ALIGN", 4: "BL_ERR_DTYPE",
     5: "BL_ERR_WORKSPACE", 6: "BL_ERR_UNSUPPORTED", 7: "BL_ERR_CUDA", 8: "BL_ERR_TIMEOUT",
-    9: "BL_ERR_BAD_CODE",
+    9: "BL_ERR_BAD_CODE", 10: "BL_ERR_BAD_BATCH",
 }
 BL_BF16, BL_FP32 = 0, 1
 BL_OP_PACK, BL_OP_FORWARD, BL_OP_FFN, BL_OP_VALIDATE, BL_OP_FFN_TP_UP, BL_OP_FFN_TP_DOWN = 0, 1, 2, 3, 4, 5
+BL_OP_KV4_ATTENTION = 6
 BL_GEMV_AUTO, BL_GEMV_STREAM, BL_GEMV_TENSOR, BL_GEMV_LUT = 0, 1, 2, 3
 
 # Every symbol include/bitlinear.h declares, with (restype, argtypes).
@@ -31,6 +33,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int64
 _S = ctypes.c_size_t
 _ST = ctypes.c_int
+_I32 = ctypes.c_int32
 SIGNATURES = {
     "bitlinear_status_string": (ctypes.c_char_p, [_ST]),
     "bitlinear_workspace_bytes": (_S, [ctypes.c_int, _I, _I, _I]),
@@ -52,6 +55,11 @@ SIGNATURES = {
     "bitlinear_ffn_tp_up": (_ST, [_P, _P, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P, _S, _P]),
     "bitlinear_ffn_tp_down": (_ST, [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _S, _P]),
     "bitlinear_ffn_tp_finish": (_ST, [_P, _P, _P, _P, _P, _I, _I, _P]),
+    "bitlinear_kv4_append": (_ST, [_P, _I, _P, _I, _P, _I, _I, _I32, _P, _I, _I32, _P, _P, _P, _I, _P]),
+    "bitlinear_kv4_read": (_ST, [_P, _P, _I, _P, _P, _P]),
+    "bitlinear_kv4_attention": (_ST, [_P, _I, _I, _I32, _I, ctypes.c_float, _P, _P, _P, _I, _P, _S, _P]),
+    "bitlinear_pack_weights_int8": (_ST, [_P, ctypes.c_int, _I, _I, _P, _P, _P]),
+    "bitlinear_forward_int8": (_ST, [_P, _P, _I, _I, _P, _I, _I32, _P, _P, ctypes.c_int, _P, _P, _S, _P]),
 }
 
 
@@ -266,6 +274,54 @@ def ffn(Wg, gg, Wu, gu, Wd, gd, x: torch.Tensor, residual: Optional[torch.Tensor
                              _stream(x.device))
     _check(st, "bitlinear_ffn")
     return y
+
+
+def pack_weights_int8(W: torch.Tensor):
+    """8-bit weights: W [N, K] (bf16 or fp32, CUDA) -> (Wq int8 [N, K], wstep fp32 [N])."""
+    wdt = _wdt(_cuda(W, "W"))
+    N, K = W.shape
+    Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+    wstep = torch.empty(N, dtype=torch.float32, device=W.device)
+    with torch.cuda.device(W.device):
+        st = lib().bitlinear_pack_weights_int8(_ptr(W), wdt, N, K, _ptr(Wq), _ptr(wstep), _stream(W.device))
+    _check(st, "bitlinear_pack_weights_int8")
+    return Wq, wstep
+
+
+def forward_int8(Wq: torch.Tensor, wstep: torch.Tensor, x: torch.Tensor, rmsnorm: bool = False,
+                 residual: Optional[torch.Tensor] = None, want_acc: bool = False,
+                 out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None):
+    """One 8-bit linear layer of x [M, K] bf16 (after a unit-weight RMSNorm if asked): y [M, N] in out_dtype (bf16 or
+    fp32), and the int32 accumulator with want_acc. Scratch is allocated per call unless `ws` is given."""
+    _cuda(Wq, "Wq", torch.int8)
+    _cuda(wstep, "wstep", torch.float32)
+    _cuda(x, "x", torch.bfloat16)
+    N, K = Wq.shape
+    M = x.shape[0]
+    if x.shape != (M, K) or wstep.shape != (N,):
+        raise ValueError("shapes of Wq, wstep and x do not match")
+    dev = x.device
+    if Wq.device != dev or wstep.device != dev:
+        raise ValueError("Wq, wstep and x must be on one device")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bf16 or fp32")
+    for t, name, dt in ((residual, "residual", torch.bfloat16), (out, "out", out_dtype)):
+        if t is not None and (_cuda(t, name, dt).shape != (M, N) or t.device != dev):
+            raise ValueError(f"{name} must be [{M}, {N}] on {dev}")
+    here = dev.index == torch.cuda.current_device()
+    with nullcontext() if here else torch.cuda.device(dev):
+        y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+        acc = torch.empty((M, N), dtype=torch.int32, device=dev) if want_acc else None
+        if ws is None:
+            ws = torch.empty(workspace_bytes(BL_OP_FORWARD, M, N, K), dtype=torch.uint8, device=dev)
+        st = lib().bitlinear_forward_int8(_ptr(Wq), _ptr(wstep), N, K, _ptr(x), M, int(bool(rmsnorm)), _ptr(residual),
+                                          _ptr(y), BL_FP32 if out_dtype == torch.float32 else BL_BF16, _ptr(acc),
+                                          _ptr(ws), ws.numel(), _stream(dev))
+    _check(st, "bitlinear_forward_int8")
+    return (y, acc) if want_acc else y
 
 
 def validate_packed(Wp: torch.Tensor) -> int:

@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 #define BL_API extern "C" __attribute__((visibility("default")))
 
@@ -217,6 +218,7 @@ BL_API const char* bitlinear_status_string(bl_status st) {
         case BL_ERR_UNSUPPORTED: return "BL_ERR_UNSUPPORTED: needs an sm_100 (B200) device";
         case BL_ERR_CUDA: return "BL_ERR_CUDA: a CUDA call or launch failed";
         case BL_ERR_TIMEOUT: return "BL_ERR_TIMEOUT: a bounded wait in a kernel gave up";
+        case BL_ERR_BAD_BATCH: return "BL_ERR_BAD_BATCH: a page, length or position of a batch is out of range";
         case BL_ERR_BAD_CODE: return "BL_ERR_BAD_CODE: packed weights hold the invalid code 3";
     }
     return "unknown bl_status";
@@ -236,6 +238,7 @@ BL_API size_t bitlinear_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         case BL_OP_VALIDATE: return kWsAlign;
         case BL_OP_FFN_TP_UP: return tp_up_ws(M, N, K).total;
         case BL_OP_FFN_TP_DOWN: return tp_down_ws(M, N, K).total;
+        case BL_OP_KV4_ATTENTION: return align_up(bl::kv4_attention_workspace_bytes());
         default: return 0;
     }
 }
@@ -483,7 +486,7 @@ BL_API bl_status bitlinear_get_device_error(bl_stream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return BL_ERR_CUDA;
     unsigned v = 0;
     if (bl::read_and_clear_device_error(&v) != cudaSuccess) return BL_ERR_CUDA;
-    return v ? BL_ERR_TIMEOUT : BL_OK;
+    return v & bl::kErrTimeout ? BL_ERR_TIMEOUT : v & bl::kErrBadBatch ? BL_ERR_BAD_BATCH : BL_OK;
 }
 
 // ---------------------------------------------------------------- tensor-parallel pieces
@@ -581,4 +584,132 @@ BL_API bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, co
         return BL_ERR_ALIGN;
     if (bl_status st = check_device()) return st;
     return cuda_status(bl::launch_ffn_tp_finish(acc, gd, s2, residual, y, M, d, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------- attention side
+
+namespace {
+
+// The cache and batch structs of a call, checked and turned into what the kernels take.
+bl_status kv4_args(const bl_kv4_cache* c, const bl_kv4_batch* b, int64_t M, bl::Kv4View* view, bl::Kv4Seqs* seqs) {
+    if (!c || !b) return BL_ERR_NULL;
+    if (M < 0 || M > kMaxM) return BL_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return BL_ERR_SHAPE;
+    int shift = 4;
+    while (shift < 8 && (1 << shift) != c->page_size) ++shift;
+    if ((1 << shift) != c->page_size) return BL_ERR_SHAPE;
+    if (c->num_pages < 1 || c->num_pages > INT32_MAX || c->kv_heads < 1 || c->kv_heads > 1024) return BL_ERR_SHAPE;
+    if (b->S < 1 || b->S > bl::kKv4MaxSeqs || b->W < 1 || b->table_stride < 0) return BL_ERR_SHAPE;
+    const int64_t room = (int64_t)b->W << shift;
+    if (room >= (int64_t)1 << 30 || room * b->S * c->kv_heads >= (int64_t)1 << 36) return BL_ERR_SHAPE;
+    if (M == 0) return BL_OK;
+    if (!c->kc || !c->ks || !c->vc || !c->vs || !b->q_start || !b->kv_len || !b->page_table) return BL_ERR_NULL;
+    if (!aligned(c->kc, 16) || !aligned(c->ks, 16) || !aligned(c->vc, 16) || !aligned(c->vs, 16) || !aligned(b->q_start, 4) ||
+        !aligned(b->kv_len, 4) || !aligned(b->page_table, 4))
+        return BL_ERR_ALIGN;
+    *view = bl::Kv4View{c->kc, c->ks, c->vc, c->vs, (int)c->num_pages, shift, c->kv_heads};
+    *seqs = bl::Kv4Seqs{b->q_start, b->kv_len, b->page_table, b->table_stride, b->S, b->W};
+    return BL_OK;
+}
+
+// [M, heads, D] bf16 rows `stride` elements apart, read or written 16 bytes at a time.
+bl_status rows_ok(const uint16_t* p, int64_t stride, int64_t width) {
+    if (!p) return BL_ERR_NULL;
+    if (stride < width) return BL_ERR_SHAPE;
+    if (!aligned(p, 16) || stride % 8 != 0) return BL_ERR_ALIGN;
+    return BL_OK;
+}
+
+inline bool heads_ok(int32_t Hq, int32_t hkv) { return Hq >= 1 && Hq <= 1024 && Hq % hkv == 0; }
+
+}  // namespace
+
+BL_API bl_status bitlinear_kv4_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                      const uint16_t* v, int64_t v_stride, int64_t M, int32_t Hq, const float* cos_sin,
+                                      int64_t max_pos, int32_t interleaved, const bl_kv4_cache* cache,
+                                      const bl_kv4_batch* batch, uint16_t* q_out, int64_t q_out_stride,
+                                      bl_stream_t stream) {
+    bl::Kv4View view;
+    bl::Kv4Seqs seqs;
+    if (bl_status st = kv4_args(cache, batch, M, &view, &seqs)) return st;
+    if (!heads_ok(Hq, cache->kv_heads) || max_pos < 1 || (interleaved != 0 && interleaved != 1)) return BL_ERR_SHAPE;
+    if (M == 0) return BL_OK;
+    const int64_t D = cache->head_dim;
+    if (bl_status st = rows_ok(q, q_stride, Hq * D)) return st;
+    if (bl_status st = rows_ok(k, k_stride, cache->kv_heads * D)) return st;
+    if (bl_status st = rows_ok(v, v_stride, cache->kv_heads * D)) return st;
+    if (bl_status st = rows_ok(q_out, q_out_stride, Hq * D)) return st;
+    if (!cos_sin) return BL_ERR_NULL;
+    if (!aligned(cos_sin, 16)) return BL_ERR_ALIGN;
+    if (q_out == q && q_out_stride != q_stride) return BL_ERR_SHAPE;
+    if (bl_status st = check_device()) return st;
+    return cuda_status(bl::launch_kv4_append(q, q_stride, k, k_stride, v, v_stride, M, Hq, (int)D, cos_sin, max_pos,
+                                             interleaved, view, seqs, q_out, q_out_stride, (cudaStream_t)stream));
+}
+
+BL_API bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batch, int64_t M, uint16_t* k,
+                                    uint16_t* v, bl_stream_t stream) {
+    bl::Kv4View view;
+    bl::Kv4Seqs seqs;
+    if (bl_status st = kv4_args(cache, batch, M, &view, &seqs)) return st;
+    if (M == 0) return BL_OK;
+    if (!k || !v) return BL_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16)) return BL_ERR_ALIGN;
+    if (bl_status st = check_device()) return st;
+    return cuda_status(bl::launch_kv4_read(view, seqs, M, cache->head_dim, k, v, (cudaStream_t)stream));
+}
+
+BL_API bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int32_t Hq, int64_t max_q,
+                                         float scale, const bl_kv4_cache* cache, const bl_kv4_batch* batch, uint16_t* out,
+                                         int64_t out_stride, void* ws, size_t ws_bytes, bl_stream_t stream) {
+    bl::Kv4View view;
+    bl::Kv4Seqs seqs;
+    if (bl_status st = kv4_args(cache, batch, M, &view, &seqs)) return st;
+    if (!heads_ok(Hq, cache->kv_heads) || max_q < 0 || !(scale > 0.0f && scale <= 3.0e38f)) return BL_ERR_SHAPE;
+    if (M == 0) return BL_OK;
+    const int64_t D = cache->head_dim;
+    if (bl_status st = rows_ok(q, q_stride, Hq * D)) return st;
+    if (bl_status st = rows_ok(out, out_stride, Hq * D)) return st;
+    if (bl_status st = check_ws(ws, ws_bytes, align_up(bl::kv4_attention_workspace_bytes()))) return st;
+    if (bl_status st = check_device()) return st;
+    return cuda_status(bl::launch_kv4_attention(q, q_stride, M, Hq, (int)D, max_q, scale, view, seqs, out, out_stride, ws,
+                                                (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------- 8-bit linear layers
+
+namespace {
+constexpr int64_t kMaxK8 = 131072;  // 127 * 128 * K < 2^31
+}
+
+BL_API bl_status bitlinear_pack_weights_int8(const void* W, int wdt, int64_t N, int64_t K, int8_t* Wq, float* wstep,
+                                             bl_stream_t stream) {
+    if (wdt != BL_BF16 && wdt != BL_FP32) return BL_ERR_DTYPE;
+    if (N < 1 || N > kMaxN || K < 16 || K % 16 != 0 || K > kMaxK8) return BL_ERR_SHAPE;
+    if (!W || !Wq || !wstep) return BL_ERR_NULL;
+    if (!aligned(W, 16) || !aligned(Wq, 16) || !aligned(wstep, 4)) return BL_ERR_ALIGN;
+    if (bl_status st = check_device()) return st;
+    return cuda_status(bl::launch_pack_int8(W, wdt == BL_FP32, N, K, Wq, wstep, (cudaStream_t)stream));
+}
+
+BL_API bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x,
+                                        int64_t M, int32_t rmsnorm, const uint16_t* residual, void* y, int ydt,
+                                        int32_t* acc, void* ws, size_t ws_bytes, bl_stream_t stream) {
+    if (ydt != BL_BF16 && ydt != BL_FP32) return BL_ERR_DTYPE;
+    if (M < 0 || M > kMaxM || N < 0 || N > kMaxN || K < 16 || K % 16 != 0 || K > kMaxK8 || (rmsnorm != 0 && rmsnorm != 1))
+        return BL_ERR_SHAPE;
+    if (M == 0 || N == 0) return BL_OK;
+    if (!Wq || !wstep || !x || !y) return BL_ERR_NULL;
+    if (!aligned(Wq, 16) || !aligned(wstep, 4) || !aligned(x, 16) || !aligned(y, ydt == BL_FP32 ? 4 : 2) ||
+        (residual && !aligned(residual, 2)) || (acc && !aligned(acc, 4)))
+        return BL_ERR_ALIGN;
+    const ForwardWs w = forward_ws(M, N, K);
+    if (bl_status st = check_ws(ws, ws_bytes, w.total)) return st;
+    if (bl_status st = check_device()) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    int8_t* xq = (int8_t*)((char*)ws + w.xq);
+    float* scale = (float*)((char*)ws + w.scale);
+    BL_TRY(bl::launch_act_quant(x, M, K, bl::XQ_NATURAL, xq, scale, nullptr, s, rmsnorm != 0));
+    return cuda_status(bl::launch_int8(Wq, wstep, N, K, xq, scale, M, residual, ydt == BL_BF16 ? (uint16_t*)y : nullptr,
+                                       ydt == BL_FP32 ? (float*)y : nullptr, acc, s));
 }

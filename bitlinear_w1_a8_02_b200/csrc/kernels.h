@@ -151,6 +151,26 @@ cudaError_t launch_ffn_requant_parts(const float* h, const double* part_ss, cons
 cudaError_t launch_ffn_tp_finish(const int32_t* acc, const float* gd, const float* s2, const uint16_t* residual,
                                  uint16_t* y, int64_t M, int64_t d, cudaStream_t s);
 
+// ---- 4-bit paged cache (kv4.cu) and the attention over it (kv4_attn.cu); the
+// structs are in kv4.cuh
+struct Kv4View;
+struct Kv4Seqs;
+cudaError_t launch_kv4_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, int64_t M, int Hq, int D, const float* cos_sin, int64_t max_pos,
+                              int interleaved, const Kv4View& cache, const Kv4Seqs& batch, uint16_t* q_out,
+                              int64_t qo_stride, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t M, int D, uint16_t* k, uint16_t* v,
+                            cudaStream_t s);
+cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int Hq, int D, int64_t max_q, float scale,
+                                 const Kv4View& cache, const Kv4Seqs& batch, uint16_t* out, int64_t out_stride, void* ws,
+                                 cudaStream_t s);
+size_t kv4_attention_workspace_bytes();
+
+// ---- 8-bit linear layers (int8.cu); one of y16, y32 is set
+cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int8_t* Wq, float* wstep, cudaStream_t s);
+cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const int8_t* xq, const float* scale,
+                        int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc, cudaStream_t s);
+
 // ---- device error word: set by bounded waits inside kernels that give up.
 // Address of the current device's word (for kernels), and a host read that
 // also clears it.

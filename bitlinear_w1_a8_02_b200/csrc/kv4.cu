@@ -1,0 +1,234 @@
+// Append to and read from the 4-bit paged cache.
+//
+// Append: one pass over the new tokens' q, k and v. A lane owns an octet (8
+// consecutive dims, one 16-byte load); D/8 lanes form a vector, the key and the
+// value vector of a token and head sit side by side in one warp, so the rotation
+// partner of half-split pairs, a group's absmax (4 lanes) and the marking of a
+// token with a non-finite value are warp shuffles and a ballot. A lane's 8 codes
+// are one 32-bit word of the packed vector.
+//
+// Bound by DRAM: per token 2 (Hq + 2 Hkv) D bytes in, 2 Hq D + Hkv (D + D/8) out;
+// the rotation row (4 D bytes) is read by every head of a token, so from L1.
+#include "kv4.cuh"
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, qo_stride;
+    uint16_t* q_out;
+    const float* cos_sin;
+    int64_t max_pos;
+    Kv4View cache;
+    Kv4Seqs batch;
+    int M, Hq, warps_per_token;
+    int interleaved;
+    unsigned* err;
+};
+
+__device__ __forceinline__ void unpack_octet(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+
+// Rotate the octet `o` (dims 8 o ..) of a vector held by D/8 adjacent lanes. Every
+// lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void rotate_octet(const uint4& raw, int o, const float* row, bool interleaved, float (&r)[8]) {
+    constexpr int LPV = D / 8;
+    float x[8];
+    unpack_octet(raw, x);
+    if (interleaved) {
+        const float4 c = *reinterpret_cast<const float4*>(row + 4 * o);
+        const float4 s = *reinterpret_cast<const float4*>(row + D / 2 + 4 * o);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = x[2 * j], b = x[2 * j + 1];
+            r[2 * j] = __fsub_rn(__fmul_rn(a, cc[j]), __fmul_rn(b, ss[j]));
+            r[2 * j + 1] = __fadd_rn(__fmul_rn(b, cc[j]), __fmul_rn(a, ss[j]));
+        }
+        return;
+    }
+    uint4 other;
+    other.x = __shfl_xor_sync(0xffffffffu, raw.x, LPV / 2);
+    other.y = __shfl_xor_sync(0xffffffffu, raw.y, LPV / 2);
+    other.z = __shfl_xor_sync(0xffffffffu, raw.z, LPV / 2);
+    other.w = __shfl_xor_sync(0xffffffffu, raw.w, LPV / 2);
+    float p[8];
+    unpack_octet(other, p);
+    const bool low = o < LPV / 2;  // this lane holds the a of its pairs
+    const int i = 8 * (o & (LPV / 2 - 1));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * h);
+        const float4 s = *reinterpret_cast<const float4*>(row + D / 2 + i + 4 * h);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float own = __fmul_rn(x[4 * h + j], cc[j]), oth = __fmul_rn(p[4 * h + j], ss[j]);
+            r[4 * h + j] = low ? __fsub_rn(own, oth) : __fadd_rn(own, oth);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+    constexpr int LPV = D / 8;  // lanes of a vector
+    constexpr int G = D / kKvGroup;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t gw = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int m = (int)(gw / a.warps_per_token);
+    if (m >= a.M) return;
+    const int item = (int)(gw % a.warps_per_token) * 32 + lane;  // lane of the token
+
+    const int s = kv4_seq_of_row(a.batch, m);
+    if (s >= a.batch.S) return;  // padding
+    const int n_end = a.batch.q_start[s + 1], len = a.batch.kv_len[s];
+    const int64_t pos = (int64_t)len - n_end + m;
+    if (len < 0 || m < a.batch.q_start[s] || n_end > a.M || pos >= a.max_pos ||
+        pos >= ((int64_t)a.batch.W << a.cache.page_shift)) {
+        if (lane == 0) atomicOr(a.err, kErrBadBatch);
+        return;
+    }
+    if (pos < 0) return;  // no place in the cache: padding of an idle sequence
+    const float* row = a.cos_sin + pos * D;
+    const int kv_lanes = 2 * LPV * a.cache.hkv;
+    const bool is_kv = item < kv_lanes;
+    const bool is_q = !is_kv && item < kv_lanes + LPV * a.Hq;
+    const int o = item % LPV;  // octet of the vector
+    const int vec = is_kv ? item / LPV : (item - kv_lanes) / LPV;
+    const bool is_v = is_kv && (vec & 1);
+    const int head = is_kv ? vec >> 1 : vec;
+
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (is_kv)
+        raw = *reinterpret_cast<const uint4*>((is_v ? a.v + m * a.v_stride : a.k + m * a.k_stride) + head * D + 8 * o);
+    else if (is_q)
+        raw = *reinterpret_cast<const uint4*>(a.q + m * a.q_stride + head * D + 8 * o);
+    float x[8];
+    rotate_octet<D>(raw, o, row, a.interleaved != 0, x);
+    if (is_q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = f32_to_bf16_bits(x[2 * j]) | (uint32_t)f32_to_bf16_bits(x[2 * j + 1]) << 16;
+        *reinterpret_cast<uint4*>(a.q_out + m * a.qo_stride + head * D + 8 * o) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // a warp without key or value lanes is done; the others stay together for the shuffles
+    if (!__any_sync(0xffffffffu, is_kv)) return;
+    if (is_v) unpack_octet(raw, x);
+    bool bad = false;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        bad |= !(fabsf(x[j]) < kKvHuge);
+        top = fmaxf(top, fabsf(x[j]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const unsigned votes = __ballot_sync(0xffffffffu, bad && is_kv);
+    if (!is_kv) return;
+    // the key and value lanes of this token and head
+    const unsigned mine = LPV == 16 ? 0xffffffffu : 0xffffu << (lane & 16);
+    const bool marked = (votes & mine) != 0;
+    const float step = marked ? 0.0f : kv4_step(top);
+    const uint32_t word = kv4_word(x, step, !marked);
+    const int64_t at = kv4_vector(a.cache, a.batch, s, (int)pos, head);
+    if (at < 0) {
+        atomicOr(a.err, kErrBadBatch);
+        return;
+    }
+    const int g = o >> 2, t = o & 3;
+    uint8_t* codes = is_v ? a.cache.vc : a.cache.kc;
+    uint16_t* steps = is_v ? a.cache.vs : a.cache.ks;
+    *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * (t * G + g)) = word;
+    if (t == 0)
+        steps[at * G + g] = marked && !is_v ? (uint16_t)0x7FC0 : (uint16_t)(__float_as_uint(step) >> 16);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4View cache, const Kv4Seqs batch, int M,
+                                                            int warps_per_token, uint16_t* k, uint16_t* v, unsigned* err) {
+    constexpr int LPV = D / 8;
+    constexpr int G = D / kKvGroup;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t gw = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int m = (int)(gw / warps_per_token);
+    if (m >= M) return;
+    const int item = (int)(gw % warps_per_token) * 32 + lane;
+    const int s = kv4_seq_of_row(batch, m);
+    if (s >= batch.S) return;
+    const int n_end = batch.q_start[s + 1];
+    const int64_t pos = (int64_t)batch.kv_len[s] - n_end + m;
+    if (batch.kv_len[s] < 0 || m < batch.q_start[s] || n_end > M || pos >= ((int64_t)batch.W << cache.page_shift)) {
+        if (lane == 0) atomicOr(err, kErrBadBatch);
+        return;
+    }
+    if (pos < 0) return;
+    if (item >= 2 * LPV * cache.hkv) return;
+    const int o = item % LPV, vec = item / LPV, head = vec >> 1;
+    const bool is_v = vec & 1;
+    const int64_t at = kv4_vector(cache, batch, s, (int)pos, head);
+    if (at < 0) {
+        atomicOr(err, kErrBadBatch);
+        return;
+    }
+    const int g = o >> 2, t = o & 3;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>((is_v ? cache.vc : cache.kc) + at * (D / 2) + 4 * (t * G + g));
+    uint32_t st = (is_v ? cache.vs : cache.ks)[at * G + g];
+    st |= st << 16;
+    const uint32_t s16 = bf16x2_mul(st, kBf16x2Sixteen), s24 = bf16x2_mul(st, kBf16x2MinusTwentyFour);
+    uint32_t p[4];  // pairs (i, i + 4)
+    p[0] = bf16x2_fma(kv4_unit_pair<0>(w), s16, s24);
+    p[1] = bf16x2_fma(kv4_unit_pair<1>(w), s16, s24);
+    p[2] = bf16x2_fma(kv4_unit_pair<2>(w), s16, s24);
+    p[3] = bf16x2_fma(kv4_unit_pair<3>(w), s16, s24);
+    const uint4 out = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                                 __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+    *reinterpret_cast<uint4*>((is_v ? v : k) + ((int64_t)m * cache.hkv + head) * D + 8 * o) = out;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, int64_t M, int Hq, int D, const float* cos_sin, int64_t max_pos,
+                              int interleaved, const Kv4View& cache, const Kv4Seqs& batch, uint16_t* q_out,
+                              int64_t qo_stride, cudaStream_t s) {
+    AppendArgs a;
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.qo_stride = qo_stride;
+    a.q_out = q_out, a.cos_sin = cos_sin, a.max_pos = max_pos;
+    a.cache = cache, a.batch = batch;
+    a.M = (int)M, a.Hq = Hq, a.interleaved = interleaved;
+    a.warps_per_token = ((2 * cache.hkv + Hq) * (D / 8) + 31) / 32;
+    cudaError_t e = device_error_word(&a.err);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (M * a.warps_per_token + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_pdl(D == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                      s, a);
+}
+
+cudaError_t launch_kv4_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t M, int D, uint16_t* k, uint16_t* v,
+                            cudaStream_t s) {
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    const int wpt = (2 * cache.hkv * (D / 8) + 31) / 32;
+    const int64_t blocks = (M * wpt + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_pdl(D == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                      cache, batch, (int)M, wpt, k, v, err);
+}
+
+}  // namespace bl

@@ -1,0 +1,109 @@
+// The 4-bit cache format and the batch description shared by the attention-side
+// kernels (append, read, attention).
+//
+// A cached value is c * step, c = n - 8 with n in 0..15 and step of five
+// significant bits. Dequantisation to bf16 is one multiply-add on pairs: with n
+// in the top four mantissa bits of 1.0, fma(1 + n/16, 16 step, -24 step) =
+// (n - 8) step; 16 step, 24 step (two more bits than step has) and the result
+// (three bits times five) are bf16 numbers, so nothing is rounded.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bl {
+
+constexpr int kKvGroup = 32;                 // dims that share a step
+constexpr int kKv4MaxSeqs = 4096;            // sequences of a batch
+constexpr unsigned kErrTimeout = 1u;         // bits of the device error word
+constexpr unsigned kErrBadBatch = 2u;
+constexpr float kKvHuge = 1.329227995784916e36f;   // 2^120: vectors that reach it are marked
+constexpr float kKvTiny = 7.888609052210118e-31f;  // 2^-100: groups below it are zero
+
+// fl(A / 7) rounded to five significant bits, ties to even.
+__device__ __forceinline__ float kv4_step(float amax) {
+    if (amax < kKvTiny) return 0.0f;
+    unsigned b = __float_as_uint(__fdiv_rn(amax, 7.0f));
+    b += 0x3FFFFu + ((b >> 19) & 1u);
+    return __uint_as_float(b & ~0x7FFFFu);
+}
+
+// Eight values -> the word of their codes (n = c + 8); `live` 0 stores c = 0.
+__device__ __forceinline__ uint32_t kv4_word(const float (&x)[8], float step, bool live) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float c = live && step > 0.0f ? rintf(__fdiv_rn(x[j], step)) : 0.0f;
+        const int n = 8 + min(max((int)c, -7), 7);
+        w |= (uint32_t)n << (4 * j);
+    }
+    return w;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Nibbles i (low half) and i + 4 (high half) of `w` as the bf16 pair 1 + n/16.
+template <int I>
+__device__ __forceinline__ uint32_t kv4_unit_pair(uint32_t w) {
+    const uint32_t sh = I == 0 ? w << 3 : w >> (4 * I - 3);
+    return (sh & 0x00780078u) | 0x3F803F80u;
+}
+
+constexpr uint32_t kBf16x2Sixteen = 0x41804180u;    // (16, 16)
+constexpr uint32_t kBf16x2MinusTwentyFour = 0xC1C0C1C0u;  // (-24, -24)
+
+// The public structs as the kernels take them.
+struct Kv4View {
+    uint8_t* kc;
+    uint16_t* ks;
+    uint8_t* vc;
+    uint16_t* vs;
+    int num_pages;
+    int page_shift;  // page size = 1 << page_shift
+    int hkv;
+};
+
+struct Kv4Seqs {
+    const int* q_start;
+    const int* kv_len;
+    const int* table;
+    int64_t table_stride;
+    int S;
+    int W;
+};
+
+// Vector index ((page * Hkv + head) * P + offset) of position `pos` of sequence s.
+// The caller has checked pos < W * P; a page id out of range gives -1.
+__device__ __forceinline__ int64_t kv4_vector(const Kv4View& c, const Kv4Seqs& b, int s, int pos, int head) {
+    const int page = b.table[s * b.table_stride + (pos >> c.page_shift)];
+    if (page < 0 || page >= c.num_pages) return -1;
+    return ((((int64_t)page * c.hkv + head) << c.page_shift)) + (pos & ((1 << c.page_shift) - 1));
+}
+
+// Sequence that row `m` belongs to (S: none, a padding row); all 32 lanes call it.
+__device__ __forceinline__ int kv4_seq_of_row(const Kv4Seqs& b, int m) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int s0 = 0; s0 < b.S; s0 += 32) {
+        const bool before = s0 + lane < b.S && b.q_start[s0 + lane + 1] <= m;
+        const int k = __popc(__ballot_sync(0xffffffffu, before));
+        n += k;
+        if (k < 32) break;
+    }
+    return min(n, b.S);
+}
+
+}  // namespace bl

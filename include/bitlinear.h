@@ -72,7 +72,8 @@ typedef enum {
     BL_ERR_UNSUPPORTED = 6, /* valid arguments this build does not handle (e.g. no sm_100 device) */
     BL_ERR_CUDA = 7,        /* a CUDA call or launch failed */
     BL_ERR_TIMEOUT = 8,     /* a bounded wait inside a kernel gave up (see bitlinear_get_device_error) */
-    BL_ERR_BAD_CODE = 9     /* packed weights hold the invalid code 3 */
+    BL_ERR_BAD_CODE = 9,    /* packed weights hold the invalid code 3 */
+    BL_ERR_BAD_BATCH = 10   /* a kernel met a page, length or position out of range (see bitlinear_get_device_error) */
 } bl_status;
 
 typedef enum { BL_BF16 = 0, BL_FP32 = 1 } bl_dtype;
@@ -84,7 +85,8 @@ typedef enum {
     BL_OP_FFN = 2,      /* sizes: M, N = f (hidden), K = d (model width) */
     BL_OP_VALIDATE = 3, /* sizes ignored */
     BL_OP_FFN_TP_UP = 4,    /* sizes: M, N = f_local (the rank's hidden columns), K = d */
-    BL_OP_FFN_TP_DOWN = 5   /* sizes: M, N = d, K = f_local */
+    BL_OP_FFN_TP_DOWN = 5,  /* sizes: M, N = d, K = f_local */
+    BL_OP_KV4_ATTENTION = 6 /* sizes ignored */
 } bl_op;
 
 /* Kernels for M <= 16 tokens (bitlinear_set_gemv_kernel). */
@@ -353,6 +355,149 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
                                   uint16_t* y, int64_t M, int64_t d, bl_stream_t stream);
 
 /*
+ * Attention with keys and values held in 4 bits in a paged cache: the part of a
+ * decoder block between its Q/K/V projections (bitlinear_forward_ex) and its
+ * output projection. The pages name the block's linear layers and norms only
+ * (paper card "BitNet b1.58 2B4T Technical Report", "Method Adaptation"); the
+ * cache format is this library's.
+ *
+ * Quantisation. A vector (one token, one key/value head, D dims) is cut into
+ * groups of 32 consecutive dims. With A = max |x| of a group:
+ *   step = fl(A / 7) rounded to five significant bits (nearest, ties to even);
+ *          0 where A < 2^-100
+ *   c    = rint(fl(x / step))  in [-7, 7];  0 where step = 0
+ * The value held is c * step, a bf16 number exactly. A key or value vector with
+ * a NaN, an infinity or a magnitude of 2^120 or more marks its token in that
+ * head: the key steps become NaN, the value steps and all codes 0, so every
+ * query that sees the token is NaN in the heads that share it, and no other is.
+ *
+ * Cache. Pages of P tokens, four arrays:
+ *   kc, vc  [num_pages, Hkv, P, D/2] uint8   codes n = c + 8, two per byte
+ *   ks, vs  [num_pages, Hkv, P, D/32] bf16   steps
+ * The D/2 bytes of a vector are D/8 little-endian 32-bit words; word
+ * t * (D/32) + g holds dims 32 g + 8 t .. + 7, the j-th in bits 4j .. 4j+3.
+ * Steps of values in tokens that are attended to must be finite (those that
+ * bitlinear_kv4_append writes are).
+ *
+ * Batch. S sequences, their new tokens stacked in M rows:
+ *   q_start     [S + 1] device int32: rows q_start[s] .. q_start[s+1] - 1 belong to
+ *               sequence s; not decreasing, q_start[0] = 0, q_start[S] <= M. Rows at or after
+ *               q_start[S] are padding: nothing is read for them or written to them.
+ *   kv_len      [S] device int32: tokens of the sequence in the cache, the new
+ *               ones included. New token i of n has position kv_len - n + i; one
+ *               whose position is negative (an idle sequence, kv_len 0) is not
+ *               stored, its row is left as it was, and its attention output is zero.
+ *   page_table  [S, W] device int32, rows table_stride elements apart: page of the
+ *               tokens w P .. w P + P - 1. Entries past the last token are not read.
+ * A page may stand in several rows (a shared prefix) where it is only read; the
+ * tokens that a call appends must not share a slot.
+ * The arrays live on the device, so their contents are checked by the kernels:
+ * a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P, a
+ * q_start that leaves 0 .. M, or a position past the rotation table sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
+ * access leaves the buffers, and the rows concerned are unspecified.
+ *
+ * Sizes for all calls: D 64 or 128; P 16, 32, 64, 128 or 256; 1 <= S <= 4096;
+ * Hq % Hkv == 0, Hq <= 1024; M <= 65535; W >= 1, W P < 2^30, S Hkv W P < 2^36;
+ * 1 <= num_pages < 2^31.
+ */
+typedef struct {
+    uint8_t* kc;        /* 16-byte aligned, as the other three */
+    uint16_t* ks;
+    uint8_t* vc;
+    uint16_t* vs;
+    int64_t num_pages;
+    int32_t page_size;  /* P */
+    int32_t kv_heads;   /* Hkv */
+    int32_t head_dim;   /* D */
+} bl_kv4_cache;
+
+typedef struct {
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int64_t table_stride;
+    int32_t S;
+    int32_t W;
+} bl_kv4_batch;
+
+/*
+ * Rotate the queries and keys of the batch's new tokens and store keys and
+ * values in the cache. With position p and the pair (a, b) of dims:
+ *   a' = fl(fl(a cos) - fl(b sin)),  b' = fl(fl(b cos) + fl(a sin))
+ * Keys are quantised from the fp32 a', b'; values from their bf16.
+ *   q, k, v     [M, Hq | Hkv | Hkv, D] device bf16; row m of x at x + m * x_stride
+ *               elements, heads side by side (the column blocks of a stacked
+ *               projection fit as they are); 16-byte aligned, strides multiples of 8
+ *   q_out       rotated queries, bf16, rows q_out_stride apart; may be q itself
+ *               (with the same stride)
+ *   cos_sin     [max_pos, D] device fp32: row p holds D/2 cosines, then D/2 sines;
+ *               16-byte aligned
+ *   interleaved 0: pairs (i, i + D/2); 1: pairs (2i, 2i + 1); pair i uses entry i
+ * M == 0 launches nothing.
+ */
+bl_status bitlinear_kv4_append(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                               const uint16_t* v, int64_t v_stride, int64_t M, int32_t Hq, const float* cos_sin,
+                               int64_t max_pos, int32_t interleaved, const bl_kv4_cache* cache,
+                               const bl_kv4_batch* batch, uint16_t* q_out, int64_t q_out_stride,
+                               bl_stream_t stream);
+
+/*
+ * Read the cached values of the batch's tokens back: k, v [M, Hkv, D] device
+ * bf16, 16-byte aligned, contiguous. (With q_start cumulating whole lengths this
+ * reads whole sequences.)
+ */
+bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batch, int64_t M, uint16_t* k,
+                             uint16_t* v, bl_stream_t stream);
+
+/*
+ * Causal attention of the batch's new tokens over the cache (their own keys
+ * included, so after bitlinear_kv4_append). Query head h reads key/value head
+ * h / (Hq / Hkv):
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j - max)),  j <= position
+ * on the values that the cache holds; products and sums in fp32, p_j rounded to
+ * bf16 for the product with v_j. A row that sees no key is zero.
+ *   q, out      [M, Hq, D] device bf16, rows q_stride / out_stride elements apart;
+ *               16-byte aligned, strides multiples of 8; must not overlap
+ *   max_q       the largest number of new tokens of a sequence (host): a sequence
+ *               with more is reported as BL_ERR_BAD_BATCH and left out
+ *   scale       finite, > 0 (commonly 1 / sqrt(D))
+ *   ws          bitlinear_workspace_bytes(BL_OP_KV4_ATTENTION, 0, 0, 0) bytes
+ * Deterministic: the same inputs give the same bits.
+ */
+bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int32_t Hq, int64_t max_q,
+                                  float scale, const bl_kv4_cache* cache, const bl_kv4_batch* batch, uint16_t* out,
+                                  int64_t out_stride, void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/*
+ * 8-bit weights, for the layers that BitNet b1.58 does not ternarise (the
+ * vocabulary head): one step per output row, activations quantised per token as
+ * in bitlinear_quant_act (paper card "BitNet b1.58 2B4T Technical Report",
+ * "Method Adaptation": per-token absmax to 8-bit integers).
+ *   wstep[n]   = fl(max(max_k |W[n, k]|, 1e-30) / 127)
+ *   Wq[n, k]   = clip(rint(fl(W[n, k] / wstep[n])), -127, 127)
+ * W [N, K] bf16 or fp32 as bitlinear_pack_weights (16-byte aligned), but K % 16 == 0;
+ * Wq [N, K] int8, 16-byte aligned; wstep [N] fp32.
+ */
+bl_status bitlinear_pack_weights_int8(const void* W, int wdt, int64_t N, int64_t K, int8_t* Wq, float* wstep,
+                                      bl_stream_t stream);
+
+/*
+ * One 8-bit linear layer:
+ *   xq, s  = quant(rmsnorm ? x * r : x)           as bitlinear_forward_ex
+ *   acc    = sum_k Wq[n, k] * xq[m, k]            exact int32 (K <= 131072)
+ *   y      = [residual +] fl(fl(float(acc) * wstep[n]) * fl(1 / s_m))
+ * rounded to bf16 (ydt = BL_BF16) or kept fp32 (BL_FP32: y is float).
+ *   Wq        [N, K] device int8, 16-byte aligned; N >= 0, K >= 16, K % 16 == 0
+ *   x         [M, K] device bf16, 16-byte aligned; 0 <= M <= 65535
+ *   residual  [M, N] device bf16, may be NULL; acc [M, N] device int32, may be NULL
+ *   y         [M, N], contiguous
+ *   ws        bitlinear_workspace_bytes(BL_OP_FORWARD, M, N, K) bytes
+ */
+bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x,
+                                 int64_t M, int32_t rmsnorm, const uint16_t* residual, void* y, int ydt,
+                                 int32_t* acc, void* ws, size_t ws_bytes, bl_stream_t stream);
+
+/*
  * Check packed weights for the invalid code 3. SYNCHRONISES `stream`.
  * Returns BL_OK when every code is valid, BL_ERR_BAD_CODE otherwise; the number
  * of invalid codes is written to *bad_count (host pointer, may be NULL).
@@ -362,10 +507,12 @@ bl_status bitlinear_validate_packed(const uint8_t* Wp, int64_t N, int64_t K, int
                                     void* ws, size_t ws_bytes, bl_stream_t stream);
 
 /*
- * SYNCHRONISES `stream`, then reports BL_ERR_CUDA for a pending CUDA error, or
+ * SYNCHRONISES `stream`, then reports BL_ERR_CUDA for a pending CUDA error,
  * BL_ERR_TIMEOUT when a bounded wait inside one of this library's kernels gave up
  * since the last call on this device (the kernel that gave up wrote no output it
- * could not finish and returned); the timeout flag is cleared by this call.
+ * could not finish and returned), or BL_ERR_BAD_BATCH when an attention-side
+ * kernel met a page, length or position out of range; the flags are cleared by
+ * this call.
  */
 bl_status bitlinear_get_device_error(bl_stream_t stream);
 
