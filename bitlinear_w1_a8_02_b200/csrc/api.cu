@@ -238,7 +238,8 @@ BL_API size_t bitlinear_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         case BL_OP_VALIDATE: return kWsAlign;
         case BL_OP_FFN_TP_UP: return tp_up_ws(M, N, K).total;
         case BL_OP_FFN_TP_DOWN: return tp_down_ws(M, N, K).total;
-        case BL_OP_KV4_ATTENTION: return align_up(bl::kv4_attention_workspace_bytes());
+        case BL_OP_KV4_ATTENTION:
+            return K == 64 || K == 128 ? align_up(bl::kv4_attention_workspace_bytes(std::min(M, kMaxM), std::min<int64_t>(N, 1024), (int)K)) : 0;
         default: return 0;
     }
 }
@@ -670,7 +671,9 @@ BL_API bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, in
     const int64_t D = cache->head_dim;
     if (bl_status st = rows_ok(q, q_stride, Hq * D)) return st;
     if (bl_status st = rows_ok(out, out_stride, Hq * D)) return st;
-    if (bl_status st = check_ws(ws, ws_bytes, align_up(bl::kv4_attention_workspace_bytes()))) return st;
+    max_q = std::min(max_q, M);
+    const size_t need = align_up(bl::kv4_attention_workspace_bytes(max_q, Hq / cache->kv_heads, (int)D));
+    if (bl_status st = check_ws(ws, ws_bytes, need)) return st;
     if (bl_status st = check_device()) return st;
     return cuda_status(bl::launch_kv4_attention(q, q_stride, M, Hq, (int)D, max_q, scale, view, seqs, out, out_stride, ws,
                                                 (cudaStream_t)stream));

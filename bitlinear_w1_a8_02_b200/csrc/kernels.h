@@ -164,7 +164,12 @@ cudaError_t launch_kv4_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t 
 cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int Hq, int D, int64_t max_q, float scale,
                                  const Kv4View& cache, const Kv4Seqs& batch, uint16_t* out, int64_t out_stride, void* ws,
                                  cudaStream_t s);
-size_t kv4_attention_workspace_bytes();
+size_t kv4_attention_workspace_bytes(int64_t max_q, int64_t group, int D);
+// the same for more than a few rows, on the tensor cores (kv4_tile.cu)
+cudaError_t launch_kv4_tile(const uint16_t* q, int64_t q_stride, int64_t M, int Hq, int D, int64_t max_q, float scale,
+                            const Kv4View& cache, const Kv4Seqs& batch, uint16_t* out, int64_t out_stride, void* ws,
+                            cudaStream_t s);
+size_t kv4_tile_workspace_bytes(int D);
 
 // ---- 8-bit linear layers (int8.cu); one of y16, y32 is set
 cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int8_t* Wq, float* wstep, cudaStream_t s);

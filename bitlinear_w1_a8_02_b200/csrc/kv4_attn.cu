@@ -644,21 +644,32 @@ cudaError_t launch_rows(const RowsArgs& args, int ctas_cap, cudaStream_t s) {
 
 }  // namespace
 
-// Slots of pieces, then the joins; the same for every call.
-size_t kv4_attention_workspace_bytes() {
-    return (size_t)2 * kMaxCtas * 16 * (128 + 2) * 4 + (size_t)kMaxCtas * sizeof(int4);
+namespace {
+// Rows that share a key/value head up to which the decode kernel runs.
+constexpr int64_t kRowsMax = 16;
+
+inline bool by_tiles(int64_t max_q, int64_t group) { return max_q * group > kRowsMax; }
+
+// Slots of pieces, then the joins.
+size_t rows_slots_bytes(int D) { return (size_t)2 * kMaxCtas * 16 * (D + 2) * 4; }
+}  // namespace
+
+size_t kv4_attention_workspace_bytes(int64_t max_q, int64_t group, int D) {
+    return by_tiles(max_q, group) ? kv4_tile_workspace_bytes(D) : rows_slots_bytes(D) + (size_t)kMaxCtas * sizeof(int4);
 }
 
 cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int Hq, int D, int64_t max_q, float scale,
                                  const Kv4View& cache, const Kv4Seqs& batch, uint16_t* out, int64_t out_stride, void* ws,
                                  cudaStream_t s) {
+    if (by_tiles(max_q, Hq / cache.hkv))
+        return launch_kv4_tile(q, q_stride, M, Hq, D, max_q, scale, cache, batch, out, out_stride, ws, s);
     RowsArgs a;
     a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;
     a.cache = cache, a.batch = batch;
     a.M = (int)M, a.group = Hq / cache.hkv, a.max_q = (int)std::min<int64_t>(max_q, M);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.slots = (float*)ws;
-    a.joins = (int4*)((char*)ws + (size_t)2 * kMaxCtas * 16 * (128 + 2) * 4);
+    a.joins = (int4*)((char*)ws + rows_slots_bytes(D));
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;
     const bool two = (int64_t)a.group * a.max_q > 8;

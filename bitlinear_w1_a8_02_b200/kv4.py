@@ -154,7 +154,7 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor, kv
     os = _rows(out, "out", M, Hq, D, dev)
     with _on(dev):
         if ws is None:
-            ws = torch.empty(_b.workspace_bytes(_b.BL_OP_KV4_ATTENTION, 0, 0, 0), dtype=torch.uint8, device=dev)
+            ws = torch.empty(_b.workspace_bytes(_b.BL_OP_KV4_ATTENTION, max_q, Hq // c.kv_heads, D), dtype=torch.uint8, device=dev)
         st = _b.lib().bitlinear_kv4_attention(q.data_ptr(), qs, M, Hq, int(max_q), D ** -0.5 if scale is None else scale,
                                               ctypes.byref(c), ctypes.byref(b), out.data_ptr(), os, ws.data_ptr(),
                                               ws.numel(), _b._stream(dev))

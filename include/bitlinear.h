@@ -86,7 +86,7 @@ typedef enum {
     BL_OP_VALIDATE = 3, /* sizes ignored */
     BL_OP_FFN_TP_UP = 4,    /* sizes: M, N = f_local (the rank's hidden columns), K = d */
     BL_OP_FFN_TP_DOWN = 5,  /* sizes: M, N = d, K = f_local */
-    BL_OP_KV4_ATTENTION = 6 /* sizes ignored */
+    BL_OP_KV4_ATTENTION = 6 /* sizes: M = max_q, N = Hq / Hkv, K = D */
 } bl_op;
 
 /* Kernels for M <= 16 tokens (bitlinear_set_gemv_kernel). */
@@ -461,7 +461,7 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  *   max_q       the largest number of new tokens of a sequence (host): a sequence
  *               with more is reported as BL_ERR_BAD_BATCH and left out
  *   scale       finite, > 0 (commonly 1 / sqrt(D))
- *   ws          bitlinear_workspace_bytes(BL_OP_KV4_ATTENTION, 0, 0, 0) bytes
+ *   ws          bitlinear_workspace_bytes(BL_OP_KV4_ATTENTION, max_q, Hq / Hkv, D) bytes
  * Deterministic: the same inputs give the same bits.
  */
 bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M, int32_t Hq, int64_t max_q,

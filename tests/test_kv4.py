@@ -52,7 +52,7 @@ def _call(fn, **kw):
     c = dict(kc=A, ks=A, vc=A, vs=A, num_pages=10, page_size=64, kv_heads=2, head_dim=128)
     b = dict(q_start=A, kv_len=A, page_table=A, table_stride=4, S=3, W=4)
     a = dict(q=A, q_stride=1024, k=A, k_stride=256, v=A, v_stride=256, M=3, Hq=8, cs=A, max_pos=100, il=0, out=A,
-             o_stride=1024, max_q=1, scale=0.1, ws=A, wsb=binding.workspace_bytes(bl.BL_OP_KV4_ATTENTION, 0, 0, 0),
+             o_stride=1024, max_q=1, scale=0.1, ws=A, wsb=binding.workspace_bytes(bl.BL_OP_KV4_ATTENTION, 1, 4, 128),
              cache=True, batch=True)
     for k, v in kw.items():
         next(d for d in (c, b, a) if k in d)[k] = v
@@ -93,7 +93,7 @@ def test_refusals_rows():
         assert _call("append", **kw) == want, kw
     for kw, want in ((dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("nan")), SHAPE),
                      (dict(scale=float("inf")), SHAPE), (dict(max_q=-1), SHAPE), (dict(ws=None), NULL), (dict(ws=A + 16), ALIGN),
-                     (dict(wsb=1000), WS)):
+                     (dict(wsb=1000), WS), (dict(max_q=3, Hq=16, q_stride=2048, o_stride=2048, wsb=binding.workspace_bytes(bl.BL_OP_KV4_ATTENTION, 1, 4, 128)), WS)):
         assert _call("attention", **kw) == want, kw
 
 
