@@ -25,6 +25,7 @@
 // Every wait is bounded (1 s); one that gives up sets the device error word,
 // lets the CTA drain and returns.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
@@ -39,6 +40,7 @@ constexpr int KV_STAGES = 4;      // unpacked tiles: K, V, K, V ...
 constexpr int CODE_STAGES = 3;    // packed tiles
 constexpr int THREADS = 512;
 constexpr int MAX_CTAS = 148;     // sizes the workspace
+constexpr int ITEM_UNITS = 2;     // what starting and ending an item costs, in units (it evens out the ranges)
 constexpr int SEQ_GROUP = 32;     // sequences per entry of the coarse unit table
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr float RAISE = 8.0f;
@@ -66,14 +68,18 @@ struct Cfg {
     static constexpr int SLOT = ROWS * (D + 2);           // floats of a piece
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(lbo_bytes >> 4) << 16;
-    d |= static_cast<uint64_t>(sbo_bytes >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// Low word of a shared-memory matrix descriptor (address and leading offset in
+// 16-byte units); the high word is the same for every operand here: 1024 bytes
+// between groups of 8 rows, version 1, 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // bf16 inputs, fp32 accumulators; A K-major, B K-major or MN-major.
@@ -82,19 +88,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_mn_major)
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(DESC_HI)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "r"(DESC_HI)
         : "memory");
 }
 
@@ -114,6 +120,31 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
 
@@ -144,7 +175,7 @@ __device__ __forceinline__ int blocks_of(const TileArgs& a, const Seq& w, int t)
 }
 
 __device__ __forceinline__ int units_of(const TileArgs& a, const Seq& w) {
-    int n = 0;
+    int n = w.tiles * ITEM_UNITS;
     for (int t = 0; t < w.tiles; ++t) n += blocks_of(a, w, t);
     return n * a.cache.hkv;
 }
@@ -155,26 +186,31 @@ struct Pieces {
     int s, t, head, first, blocks;  // current item, its first unit
     Seq w;
 
+    // An item spans ITEM_UNITS, then its blocks; a range that holds none of its blocks has no piece of it.
     __device__ bool next(const TileArgs& a, int& b0, int& b1) {
-        if (u >= u1) return false;
-        while (u >= first + blocks) {  // move to the item that holds u
-            first += blocks;
-            if (++head == a.cache.hkv) {
-                head = 0;
-                if (++t >= w.tiles) {
-                    t = 0;
-                    do {
-                        w = seq_of(a, ++s, false);
-                    } while (w.tiles == 0);  // a later sequence has units: u < u1 <= total
+        while (u < u1) {
+            while (u >= end()) {  // move to the item that holds u
+                first = end();
+                if (++head == a.cache.hkv) {
+                    head = 0;
+                    if (++t >= w.tiles) {
+                        t = 0;
+                        do {
+                            w = seq_of(a, ++s, false);
+                        } while (w.tiles == 0);  // a later sequence has units: u < u1 <= total
+                    }
                 }
+                blocks = blocks_of(a, w, t);
             }
-            blocks = blocks_of(a, w, t);
+            b0 = max(0, u - first - ITEM_UNITS);
+            b1 = min(blocks, u1 - first - ITEM_UNITS);
+            u = min(u1, end());
+            if (b1 > b0) return true;
         }
-        b0 = u - first;
-        b1 = min(blocks, b0 + (u1 - u));
-        u += b1 - b0;
-        return true;
+        return false;
     }
+
+    __device__ int end() const { return first + ITEM_UNITS + blocks; }
 };
 
 template <int D>
@@ -262,11 +298,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 }
                 for (p.t = 0;; ++p.t) {
                     p.blocks = blocks_of(a, p.w, p.t);
-                    if (before + p.blocks * a.cache.hkv > p.u) break;
-                    before += p.blocks * a.cache.hkv;
+                    const int n = (ITEM_UNITS + p.blocks) * a.cache.hkv;
+                    if (before + n > p.u) break;
+                    before += n;
                 }
-                p.head = (p.u - before) / p.blocks;
-                p.first = before + p.head * p.blocks;
+                p.head = (p.u - before) / (ITEM_UNITS + p.blocks);
+                p.first = before + p.head * (ITEM_UNITS + p.blocks);
                 start_sh = p;
             }
         }
@@ -287,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base_sh;
-    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + D};
+    // TMEM columns: scores of tile i at 128 i (P over them), sums of tile i at 256 + D i
     auto give_up = [&]() {
         atomicOr(a.err, kErrTimeout);
         *aborted = 1;
@@ -351,72 +388,111 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 for (uint32_t h = g > CODE_STAGES ? g - CODE_STAGES : 0; h < g; ++h)
                     tc::mbar_wait(cfull(h % CODE_STAGES), (h / CODE_STAGES) & 1, WAIT_NS);
             }
-        } else if (warp == 13 && lane == 0) {
-            // ------------------------------------------------------------ MMA issuer
+        } else if (warp == 13) {
+            // ------------------------------------------------------------ MMA issuer (the whole warp walks along;
+            // one elected lane issues)
             constexpr uint32_t id_s = idesc_bf16(TM, BLK, false);
             constexpr uint32_t id_o = idesc_bf16(TM, D, true);
             Pieces p = start_sh;
-            uint32_t n = 0;                    // blocks so far (K tile 2n, V tile 2n + 1 of the ring)
-            uint32_t np[2] = {0, 0};           // P tiles consumed
-            uint32_t nq[2] = {0, 0};           // Q tiles consumed
+            uint32_t n = 0;                // blocks so far (K tile 2n, V tile 2n + 1 of the ring)
+            uint32_t np0 = 0, np1 = 0;     // P tiles consumed
+            uint32_t nq0 = 0, nq1 = 0;     // Q tiles consumed
+            const uint32_t q_lo = desc_lo(tc::smem_u32(sQ), 16);
+            const uint32_t k_lo = desc_lo(tc::smem_u32(sT), 16), v_lo = desc_lo(tc::smem_u32(sT), C::HALF);
+            const bool leader = elect_one();
             int b0, b1;
             bool ok = true;
-            auto wait = [&](uint32_t b, uint32_t parity) { return ok && !*aborted && tc::mbar_wait(b, parity, WAIT_NS); };
-            auto scores = [&](int i, uint32_t kt) {
-                const uint64_t qd = desc_sw128(tc::smem_u32(sQ + i * C::TILE), 16, 1024);
-                const uint64_t kd = desc_sw128(tc::smem_u32(sT + (kt % KV_STAGES) * C::TILE), 16, 1024);
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                ok = ok && !*aborted && tc::mbar_wait(b, parity, WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                tc::fence_after_sync();
+                return ok;
+            };
+            auto scores = [&](auto tile, uint32_t kt) {
+                constexpr int i = decltype(tile)::value;
+                const uint32_t qd = q_lo + i * (C::TILE >> 4), kd = k_lo + (kt % KV_STAGES) * (C::TILE >> 4);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k / 4) * C::HALF + (k % 4) * 32) >> 4;
-                    mma_ss(tS[i], qd + off, kd + off, id_s, k != 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * C::HALF + (k % 4) * 32) >> 4;
+                        mma_ss(tmem + 128 * i, qd + off, kd + off, id_s, k != 0);
+                    }
+                    tc::mma_commit(sfull(i));
                 }
-                tc::mma_commit(sfull(i));
             };
-            auto values = [&](int i, uint32_t vt, bool first) {
-                const uint64_t vd = desc_sw128(tc::smem_u32(sT + (vt % KV_STAGES) * C::TILE), C::HALF, 1024);
+            auto values = [&](auto tile, uint32_t vt, bool first) {
+                constexpr int i = decltype(tile)::value;
+                const uint32_t vd = v_lo + (vt % KV_STAGES) * (C::TILE >> 4);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < BLK / 16; ++k)
-                    mma_ts(tO[i], tS[i] + 8 * k, vd + ((k * 16 * 128) >> 4), id_o, !first || k != 0);
+                    for (int k = 0; k < BLK / 16; ++k)
+                        mma_ts(tmem + 256 + i * D, tmem + 128 * i + 8 * k, vd + ((k * 16 * 128) >> 4), id_o, k != 0 || !first);
+                }
             };
+            auto commit = [&](uint32_t b) {
+                if (leader) tc::mma_commit(b);
+            };
+            using T0 = std::integral_constant<int, 0>;
+            using T1 = std::integral_constant<int, 1>;
             while (ok && p.next(a, b0, b1)) {
                 const bool two = p.w.n_q * a.group - p.t * ROWS > TM;
                 const int cnt = b1 - b0;
-                for (int j = -1; j < cnt && ok; ++j, ++n) {
+                // scores of the first block
+                uint32_t kt = 2 * n;
+                if (!wait(tfull(kt % KV_STAGES), (kt / KV_STAGES) & 1)) break;
+                if (!wait(qfull(0), nq0++ & 1)) break;
+                scores(T0{}, kt);
+                if (two) {
+                    if (!wait(qfull(1), nq1++ & 1)) break;
+                    scores(T1{}, kt);
+                }
+                commit(tempty(kt % KV_STAGES));
+                // values of block j, scores of block j + 1: tile 0, then tile 1
+                for (int j = 0; j < cnt; ++j, ++n) {
                     const bool more = j + 1 < cnt;
-                    const uint32_t vt = 2 * (n - 1) + 1, kt = 2 * n;  // V of block j, K of block j + 1
-                    if (j >= 0) ok = wait(tfull(vt % KV_STAGES), (vt / KV_STAGES) & 1);
-                    if (more) ok = wait(tfull(kt % KV_STAGES), (kt / KV_STAGES) & 1);
-                    if (!ok) break;
-#pragma unroll 1
-                    for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
-                        if (j >= 0) {
-                            ok = wait(pfull(i), np[i] & 1);
-                            if (!ok) break;
-                            ++np[i];
-                            tc::fence_after_sync();
-                            values(i, vt, j == 0);
-                            if (!more) tc::mma_commit(ofull(i));
-                        } else {
-                            ok = wait(qfull(i), nq[i] & 1);
-                            if (!ok) break;
-                            ++nq[i];
-                            tc::fence_after_sync();
-                        }
-                        if (i == (two ? 1 : 0) && j >= 0) tc::mma_commit(tempty(vt % KV_STAGES));
-                        if (more) scores(i, kt);
+                    const uint32_t vt = 2 * n + 1;
+                    kt = 2 * n + 2;
+                    if (!wait(tfull(vt % KV_STAGES), (vt / KV_STAGES) & 1)) break;
+                    if (!wait(pfull(0), np0++ & 1)) break;
+                    values(T0{}, vt, j == 0);
+                    if (!more) commit(ofull(0));
+                    if (more) {
+                        if (!wait(tfull(kt % KV_STAGES), (kt / KV_STAGES) & 1)) break;
+                        scores(T0{}, kt);
                     }
-                    if (ok && more) tc::mma_commit(tempty(kt % KV_STAGES));
-                    if (!more) break;  // n already counts this piece's blocks
+                    if (two) {
+                        if (!wait(pfull(1), np1++ & 1)) break;
+                        values(T1{}, vt, j == 0);
+                        if (!more) commit(ofull(1));
+                    }
+                    commit(tempty(vt % KV_STAGES));
+                    if (more) {
+                        if (two) scores(T1{}, kt);
+                        commit(tempty(kt % KV_STAGES));
+                    }
                 }
             }
-            if (!ok) give_up();
+            if (!ok && lane == 0) give_up();
+            __syncwarp();
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- unpack
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // A lane owns the group `gr` of a key: four words and one step. The order in which lanes take the
+        // octets makes both the word loads (32 lanes, 32 banks) and the 16-byte stores (8 lanes of a phase, 8
+        // chunks of a 128-byte row) free of bank conflicts.
         Pieces p = start_sh;
-        const int t = lane & 3;
-        const int row = (warp - 8) * 8 + (lane >> 2);  // key of the pass
+        constexpr int KPW = 32 / G;               // keys per warp and pass
+        constexpr int PASSES = BLK / (4 * KPW);
+        const int gr = lane % G;
+        const int row = (warp - 8) * KPW + lane / G;  // key of the first pass
+        int loads[4], stores[4];                  // byte offsets of the i-th octet, the same in every pass
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = D == 128 ? ((i + (row >> 1)) & 3) ^ (2 * (gr >> 1)) : (i + (row >> 2)) & 3;
+            loads[i] = row * VB + 4 * (t * G + gr);
+            stores[i] = (gr >> 1) * C::HALF + row * 128 + (((4 * (gr & 1) + t) ^ (row & 7)) << 4);
+        }
         uint32_t g = 0;
         int b0, b1;
         bool ok = true;
@@ -433,39 +509,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     }
                     const uint8_t* codes = sC + cs * C::PACKED;
                     uint8_t* tile = sT + ts * C::TILE;
+                    // all loads first: the compiler may not move one across a store to shared memory
+                    uint32_t word[PASSES][4], st[PASSES];
 #pragma unroll
-                    for (int pass = 0; pass < 4; ++pass) {
-                        const int key = pass * 32 + row;
-                        uint32_t w[G], st[G];
-                        if constexpr (D == 128) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(codes + key * VB + 16 * t);
-                            const uint2 y = *reinterpret_cast<const uint2*>(codes + C::CODES + key * 2 * G);
-                            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-                            st[0] = __byte_perm(y.x, 0, 0x1010), st[1] = __byte_perm(y.x, 0, 0x3232);
-                            st[2] = __byte_perm(y.y, 0, 0x1010), st[3] = __byte_perm(y.y, 0, 0x3232);
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(codes + key * VB + 8 * t);
-                            const uint32_t y = *reinterpret_cast<const uint32_t*>(codes + C::CODES + key * 2 * G);
-                            w[0] = x.x, w[1] = x.y;
-                            st[0] = __byte_perm(y, 0, 0x1010), st[1] = __byte_perm(y, 0, 0x3232);
-                        }
-                        if (b * BLK + key >= p.w.len) {  // behind the last token: whatever the page holds
+                    for (int pass = 0; pass < PASSES; ++pass) {
+                        st[pass] = *reinterpret_cast<const uint16_t*>(codes + C::CODES + (pass * 4 * KPW + row) * 2 * G + 2 * gr);
 #pragma unroll
-                            for (int e = 0; e < G; ++e) st[e] = 0;
-                        }
-                        // odd keys take their groups in swapped order, so that the 8 lanes of a store phase
-                        // cover all 8 chunks of a 128-byte row
-                        const bool odd = key & 1;
-                        uint8_t* base = tile + key * 128;
+                        for (int i = 0; i < 4; ++i)
+                            word[pass][i] = *reinterpret_cast<const uint32_t*>(codes + loads[i] + pass * 4 * KPW * VB);
+                    }
 #pragma unroll
-                        for (int e = 0; e < G; ++e) {
-                            const uint32_t word = odd ? w[e ^ 1] : w[e], s = odd ? st[e ^ 1] : st[e];
-                            const int gr = e ^ (odd ? 1 : 0);
-                            const uint32_t s16 = bf16x2_mul(s, kBf16x2Sixteen), s24 = bf16x2_mul(s, kBf16x2MinusTwentyFour);
-                            const uint4 o = make_uint4(bf16x2_fma(kv4_unit_pair<0>(word), s16, s24), bf16x2_fma(kv4_unit_pair<1>(word), s16, s24),
-                                                       bf16x2_fma(kv4_unit_pair<2>(word), s16, s24), bf16x2_fma(kv4_unit_pair<3>(word), s16, s24));
-                            const int chunk = 4 * (gr & 1) + t;
-                            *reinterpret_cast<uint4*>(base + (e >> 1) * C::HALF + ((chunk ^ (key & 7)) << 4)) = o;
+                    for (int pass = 0; pass < PASSES; ++pass) {
+                        // behind the last token: whatever the page holds
+                        if (b * BLK + pass * 4 * KPW + row >= p.w.len) st[pass] = 0;
+                        st[pass] = __byte_perm(st[pass], 0, 0x1010);
+                        const uint32_t s16 = bf16x2_mul(st[pass], kBf16x2Sixteen), s24 = bf16x2_mul(st[pass], kBf16x2MinusTwentyFour);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t x = word[pass][i];
+                            *reinterpret_cast<uint4*>(tile + stores[i] + pass * 4 * KPW * 128) =
+                                make_uint4(bf16x2_fma(kv4_unit_pair<0>(x), s16, s24), bf16x2_fma(kv4_unit_pair<1>(x), s16, s24),
+                                           bf16x2_fma(kv4_unit_pair<2>(x), s16, s24), bf16x2_fma(kv4_unit_pair<3>(x), s16, s24));
                         }
                     }
                     tc::mbar_arrive(cempty(cs));
@@ -476,43 +540,61 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
         }
     } else {
         // ---------------------------------------------------------------- softmax: tile i, row r of it
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int i = warp >> 2, r = tid & (TM - 1);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + D * i + lanes;
         const float sc = a.scale_log2;
         Pieces p = start_sh;
         uint32_t ns = 0, no = 0;
         int4 join = make_int4(0, 0, 0, -1);
-        int b0, b1;
-        bool ok = true;
-        while (ok && p.next(a, b0, b1)) {
-            const int rows = min(ROWS, p.w.n_q * a.group - p.t * ROWS);
-            const bool starts = b0 == 0, ends = b1 == p.blocks;
-            if (starts && !ends) {
-                const int item_end = p.first + p.blocks;
-                const int last = (int)(((long long)item_end * ctas + total - 1) / total) - 1;
-                join = make_int4(p.w.row0, p.head, p.t | (rows << 20), last);
-            }
-            if (i * TM >= rows) continue;
-            const int ri = p.t * ROWS + i * TM + r;  // row of the sequence
-            const bool live = i * TM + r < rows;
-            const int token = ri / a.group, qh = p.head * a.group + ri % a.group;
-            const int limit = live ? min(p.w.len, p.w.len - p.w.n_q + token + 1) : 0;
-            const int least = p.w.len - p.w.n_q + (p.t * ROWS + i * TM) / a.group + 1;  // keys all rows see
-            {   // this row's queries -> shared memory
-                const uint16_t* qp = a.q + (live ? (int64_t)(p.w.row0 + token) * a.q_stride + qh * D : 0);
-                uint8_t* dst = sQ + i * C::TILE + r * 128;
-#pragma unroll
-                for (int o = 0; o < D / 8; ++o) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (live) x = *reinterpret_cast<const uint4*>(qp + 8 * o);
-                    const uint4 y = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                    *reinterpret_cast<uint4*>(dst + (o >> 3) * C::HALF + (((o & 7) ^ (r & 7)) << 4)) = y;
+        constexpr int LPR = D / 8, RPI = 32 / LPR, QN = 32 / RPI;  // lanes of a row, rows and count of 16-byte accesses
+        const int oct = lane % LPR;
+        // The next piece that has rows in this tile: what the thread needs to know of it, and the warp's 32 rows of
+        // queries on their way into registers, D / 8 lanes to a row.
+        int b0 = 0, b1 = 0, limit = 0, least = 0;
+        int64_t row_out = -1;  // this row's offset in out, -1 for a row that does not exist
+        bool starts = false, ends = false;
+        uint4 qv[QN];
+        auto fetch = [&]() {
+            int rows;
+            do {
+                if (!p.next(a, b0, b1)) return false;
+                rows = min(ROWS, p.w.n_q * a.group - p.t * ROWS);
+                starts = b0 == 0, ends = b1 == p.blocks;
+                if (starts && !ends) {
+                    const int last = (int)(((long long)p.end() * ctas + total - 1) / total) - 1;
+                    join = make_int4(p.w.row0, p.head, p.t | (rows << 20), last);
                 }
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(qfull(i));
+            } while (i * TM >= rows);
+            const bool live = i * TM + r < rows;
+            const int ri = p.t * ROWS + i * TM + r;  // row of the sequence
+            const int token = ri / a.group, qh = p.head * a.group + ri % a.group;
+            limit = live ? min(p.w.len, p.w.len - p.w.n_q + token + 1) : 0;
+            least = p.w.len - p.w.n_q + (p.t * ROWS + i * TM) / a.group + 1;  // keys all rows see
+            row_out = live ? (int64_t)(p.w.row0 + token) * a.out_stride + qh * D : -1;
+            const int64_t qoff = live ? (int64_t)(p.w.row0 + token) * a.q_stride + qh * D : -1;
+#pragma unroll
+            for (int x = 0; x < QN; ++x) {
+                const int64_t off = __shfl_sync(0xffffffffu, qoff, x * RPI + lane / LPR);
+                qv[x] = make_uint4(0, 0, 0, 0);
+                if (off >= 0) qv[x] = *reinterpret_cast<const uint4*>(a.q + off + 8 * oct);
             }
+            return true;
+        };
+        bool ok = true;
+        bool have = fetch();
+        while (have) {
+#pragma unroll
+            for (int x = 0; x < QN; ++x) {
+                const int rr = (warp & 3) * 32 + x * RPI + lane / LPR;
+                const uint4 v = qv[x];
+                *reinterpret_cast<uint4*>(sQ + i * C::TILE + (oct >> 3) * C::HALF + rr * 128 + (((oct & 7) ^ (rr & 7)) << 4)) =
+                    make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632));
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(qfull(i));
             float mx = -INFINITY, thr = -INFINITY, msc = 0.0f, den = 0.0f;
             for (int b = b0; b < b1; ++b, ++ns) {
                 ok = !*aborted && tc::mbar_wait(sfull(i), ns & 1, WAIT_NS);
@@ -521,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 tc::fence_after_sync();
                 uint32_t s[4][32];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc::tmem_ld_32x32(tS[i] + lanes + 32 * k, s[k]);
+                for (int k = 0; k < 4; ++k) tc::tmem_ld_32x32(tS + 32 * k, s[k]);
                 tc::tmem_ld_wait();
                 if (b * BLK + BLK > least) {
                     const int seen = limit - b * BLK;  // columns this row sees
@@ -533,10 +615,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
+                for (int x = 0; x < 32; x += 2)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], __uint_as_float(s[k][x]));
-                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], __uint_as_float(s[k][x]), __uint_as_float(s[k][x + 1]));
+                const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
                 const bool raise = m > thr;
                 if (__any_sync(0xffffffffu, raise)) {
                     float f = 1.0f;
@@ -552,35 +634,41 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
 #pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
                             uint32_t o[32];
-                            tc::tmem_ld_32x32(tO[i] + lanes + 32 * k, o);
+                            tc::tmem_ld_32x32(tO + 32 * k, o);
                             tc::tmem_ld_wait();
 #pragma unroll
                             for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tc::tmem_st_32x32(tO[i] + lanes + 32 * k, o);
+                            tc::tmem_st_32x32(tO + 32 * k, o);
                         }
                     }
                 }
-                float d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-msc, -msc);
+                float2 d2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
                         const int k = 2 * h + (x >> 4), y = 2 * (x & 15);
-                        const float p0 = exp2_approx(fmaf(__uint_as_float(s[k][y]), sc, -msc));
-                        const float p1 = exp2_approx(fmaf(__uint_as_float(s[k][y + 1]), sc, -msc));
-                        d4[2 * (x & 1)] += p0;
-                        d4[2 * (x & 1) + 1] += p1;
-                        pk[x] = pack_bf16(p0, p1);
+                        float2 e = fma2(make_float2(__uint_as_float(s[k][y]), __uint_as_float(s[k][y + 1])), sc2, off2);
+                        e.x = exp2_approx(e.x);
+                        e.y = exp2_approx(e.y);
+                        d2[x & 1] = add2(d2[x & 1], e);
+                        pk[x] = pack_bf16(e.x, e.y);
                     }
-                    tc::tmem_st_32x32(tS[i] + lanes + 32 * h, pk);
+                    tc::tmem_st_32x32(tS + 32 * h, pk);
                 }
-                den += (d4[0] + d4[1]) + (d4[2] + d4[3]);
+                den += (d2[0].x + d2[0].y) + (d2[1].x + d2[1].y);
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 tc::mbar_arrive(pfull(i));
             }
+            // this piece's rows, before the next piece's take their place; its queries load during the last product
+            const bool whole = starts && ends;
+            const int64_t row = row_out;
+            const size_t slot_at = (size_t)(2 * c + (starts ? 1 : 0)) * C::SLOT;
             if (ok) {
+                have = fetch();
                 ok = !*aborted && tc::mbar_wait(ofull(i), no & 1, WAIT_NS);
                 ok = __all_sync(0xffffffffu, ok);
                 ++no;
@@ -590,16 +678,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 break;
             }
             tc::fence_after_sync();
-            const bool whole = starts && ends;
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-            float4* slot = reinterpret_cast<float4*>(a.slots + (size_t)(2 * c + (starts ? 1 : 0)) * C::SLOT) + i * TM + r;
-            uint16_t* op = a.out + (live ? (int64_t)(p.w.row0 + token) * a.out_stride + qh * D : 0);
+            float4* slot = reinterpret_cast<float4*>(a.slots + slot_at) + i * TM + r;
+            // whole rows go out through the tile's query memory, which no MMA reads any more
+            uint8_t* stage = sQ + i * C::TILE;
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
-                tc::tmem_ld_32x32(tO[i] + lanes + 32 * k, o);
+                tc::tmem_ld_32x32(tO + 32 * k, o);
                 tc::tmem_ld_wait();
-                if (!live) continue;
 #pragma unroll
                 for (int x = 0; x < 32; x += 8) {
                     float f[8];  // back in order: column 2j is dim j, column 2j + 1 dim j + 4
@@ -611,15 +698,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     if (whole) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] *= inv;
-                        *reinterpret_cast<uint4*>(op + 32 * k + x) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                        const int o8 = 4 * k + x / 8;
+                        *reinterpret_cast<uint4*>(stage + (o8 >> 3) * C::HALF + r * 128 + (((o8 & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
                     } else {
                         slot[(8 * k + x / 4) * ROWS] = make_float4(f[0], f[1], f[2], f[3]);
                         slot[(8 * k + x / 4 + 1) * ROWS] = make_float4(f[4], f[5], f[6], f[7]);
                     }
                 }
             }
-            if (!whole && live) {
-                float2* st = reinterpret_cast<float2*>(a.slots + (size_t)(2 * c + (starts ? 1 : 0)) * C::SLOT + ROWS * D) + i * TM + r;
+            if (whole) {
+                __syncwarp();
+#pragma unroll 4
+                for (int x = 0; x < 32 / RPI; ++x) {
+                    const int from = x * RPI + lane / LPR, rr = (warp & 3) * 32 + from;
+                    const int64_t off = __shfl_sync(0xffffffffu, row, from);
+                    if (off >= 0)
+                        *reinterpret_cast<uint4*>(a.out + off + 8 * oct) =
+                            *reinterpret_cast<const uint4*>(stage + (oct >> 3) * C::HALF + rr * 128 + (((oct & 7) ^ (rr & 7)) << 4));
+                }
+                __syncwarp();  // before the next item's queries overwrite the rows
+            } else {
+                float2* st = reinterpret_cast<float2*>(a.slots + slot_at + ROWS * D) + i * TM + r;
                 *st = make_float2(mx == -INFINITY ? -INFINITY : msc, den);
             }
         }
@@ -630,9 +730,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 13) {
-        if (lane == 0 && abort_sh) {
+        if (abort_sh) {
             // no MMA may still be using TMEM when it is released
-            tc::mma_commit(drained);
+            if (elect_one()) tc::mma_commit(drained);
             tc::mbar_wait(drained, 0, WAIT_NS);
         }
         __syncwarp();
