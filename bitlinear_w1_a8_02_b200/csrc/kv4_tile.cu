@@ -36,14 +36,20 @@ namespace {
 constexpr int BLK = 128;          // keys per unit
 constexpr int TM = 128;           // rows per tile
 constexpr int ROWS = 2 * TM;      // rows per item
-constexpr int KV_STAGES = 4;      // unpacked tiles: K, V, K, V ...
+constexpr int KV_STAGES = 4;      // unpacked tiles: K, V, K, V
 constexpr int CODE_STAGES = 3;    // packed tiles
-constexpr int THREADS = 512;
+constexpr int SOFT_WARPS = 8;     // two tiles x four warps
+constexpr int UNPACK_WARPS = 8;
+constexpr int LOAD_WARP = SOFT_WARPS + UNPACK_WARPS, MMA_WARP = LOAD_WARP + 1;
+constexpr int THREADS = 32 * (LOAD_WARP + 4);
+// registers a thread, per warpgroup: two of softmax, two of unpacking, one of the rest (launched with 96)
+constexpr int LAUNCH_REGS = 96, SOFT_REGS = 160, UNPACK_REGS = 48, REST_REGS = 56;
+static_assert(2 * SOFT_REGS + 2 * UNPACK_REGS + REST_REGS <= 5 * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536, "register split");
 constexpr int MAX_CTAS = 148;     // sizes the workspace
 constexpr int ITEM_UNITS = 2;     // what starting and ending an item costs, in units (it evens out the ranges)
 constexpr int SEQ_GROUP = 32;     // sequences per entry of the coarse unit table
 constexpr uint64_t WAIT_NS = 1000000000ull;
-constexpr float RAISE = 8.0f;
+constexpr float RAISE_SUM = 1024.0f;  // sum of a row's exponentials over a block that raises its maximum
 
 struct TileArgs {
     const uint16_t* q;
@@ -148,6 +154,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// 2^x of two values on the multiply-add pipe, for a share of the exponentials
+// (the special-function pipe alone would take as long as the MMAs): x = n + f,
+// |f| <= 1/2, by adding 1.5 * 2^23; 2^f by a cubic (fitted to the least largest
+// relative error, 7.5e-05, a fraction of a bf16 rounding); 2^n as an exponent.
+// x below -127 gives 0, a NaN stays one.
+constexpr int POLY_EVERY = 0;
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
+    const float2 magic = make_float2(12582912.0f, 12582912.0f), minus = make_float2(-12582912.0f, -12582912.0f);
+    const float2 t = add2(x, magic);
+    const float2 n = add2(t, minus);
+    const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
+    float2 y = fma2(f, make_float2(0.0551713221f, 0.0551713221f), make_float2(0.242610544f, 0.242610544f));
+    y = fma2(y, f, make_float2(0.693260968f, 0.693260968f));
+    y = fma2(y, f, make_float2(0.999928117f, 0.999928117f));
+    y.x *= __uint_as_float((__float_as_uint(t.x) << 23) + 0x3F800000u);
+    y.y *= __uint_as_float((__float_as_uint(t.y) << 23) + 0x3F800000u);
+    return y;
+}
+
 // A sequence's share of the work.
 struct Seq {
     int row0, n_q, len, tiles;
@@ -226,6 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     __shared__ int coarse[kKv4MaxSeqs / SEQ_GROUP + 1];  // units before each group of sequences
     __shared__ Pieces start_sh;
     __shared__ int total_sh;
+    __shared__ int valid_sh[CODE_STAGES];  // keys of a packed tile, -1 after the last
 
     uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sT = sQ + 2 * C::TILE;
@@ -245,8 +273,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < KV_STAGES; ++i) tc::mbar_init(tfull(i), 128), tc::mbar_init(tempty(i), 1);
-        for (int i = 0; i < CODE_STAGES; ++i) tc::mbar_init(cfull(i), 1), tc::mbar_init(cempty(i), 128);
+        for (int i = 0; i < KV_STAGES; ++i) tc::mbar_init(tfull(i), 32 * UNPACK_WARPS), tc::mbar_init(tempty(i), 1);
+        for (int i = 0; i < CODE_STAGES; ++i) tc::mbar_init(cfull(i), 1), tc::mbar_init(cempty(i), 32 * UNPACK_WARPS);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(sfull(i), 1);
             tc::mbar_init(pfull(i), 128);
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
         if (tid == 0) a.joins[c] = make_int4(0, 0, 0, -1);
         return;
     }
-    if (warp == 13) {
+    if (warp == MMA_WARP) {
         tc::tmem_alloc(tc::smem_u32(&tmem_base_sh), 512);
         tc::tmem_relinquish();
     }
@@ -324,15 +352,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base_sh;
-    // TMEM columns: scores of tile i at 128 i (P over them), sums of tile i at 256 + D i
+    // TMEM columns: scores of tile i at 128 i (P over their first half), sums of tile i at 256 + D i
     auto give_up = [&]() {
         atomicOr(a.err, kErrTimeout);
         *aborted = 1;
     };
 
-    if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 12) {
+    if (warp >= LOAD_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REST_REGS));
+        if (warp == LOAD_WARP) {
             // ------------------------------------------------------------ loader
             // the cache may have been written by ordinary stores of the kernel before
             asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -367,6 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         if (g >= CODE_STAGES) ok = tc::mbar_wait(cempty(st), (g / CODE_STAGES - 1) & 1, WAIT_NS);
                         ok = __all_sync(0xffffffffu, ok && !*aborted);
                         if (!ok) break;
+                        if (lane == 0) valid_sh[st] = max(0, p.w.len - b * BLK);
                         if (lane == 0) tc::mbar_arrive_expect_tx(cfull(st), live * part_keys * (VB + 2 * G));
                         __syncwarp();
                         const int part = lane >> 1, steps = lane & 1;
@@ -382,13 +411,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     }
                 }
             }
+            if (ok) {  // tell the unpackers that this was all
+                const int st = g % CODE_STAGES;
+                if (g >= CODE_STAGES) ok = tc::mbar_wait(cempty(st), (g / CODE_STAGES - 1) & 1, WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && lane == 0) {
+                    valid_sh[st] = -1;
+                    tc::mbar_arrive(cfull(st));
+                }
+            }
             if (!ok && lane == 0) {
                 give_up();
                 // let the copies still in flight land before the CTA exits
                 for (uint32_t h = g > CODE_STAGES ? g - CODE_STAGES : 0; h < g; ++h)
                     tc::mbar_wait(cfull(h % CODE_STAGES), (h / CODE_STAGES) & 1, WAIT_NS);
             }
-        } else if (warp == 13) {
+        } else if (warp == MMA_WARP) {
             // ------------------------------------------------------------ MMA issuer (the whole warp walks along;
             // one elected lane issues)
             constexpr uint32_t id_s = idesc_bf16(TM, BLK, false);
@@ -403,89 +441,92 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             int b0, b1;
             bool ok = true;
             auto wait = [&](uint32_t b, uint32_t parity) {
-                ok = ok && !*aborted && tc::mbar_wait(b, parity, WAIT_NS);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = tc::mbar_wait(b, parity, WAIT_NS);
                 tc::fence_after_sync();
                 return ok;
-            };
-            auto scores = [&](auto tile, uint32_t kt) {
-                constexpr int i = decltype(tile)::value;
-                const uint32_t qd = q_lo + i * (C::TILE >> 4), kd = k_lo + (kt % KV_STAGES) * (C::TILE >> 4);
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * C::HALF + (k % 4) * 32) >> 4;
-                        mma_ss(tmem + 128 * i, qd + off, kd + off, id_s, k != 0);
-                    }
-                    tc::mma_commit(sfull(i));
-                }
-            };
-            auto values = [&](auto tile, uint32_t vt, bool first) {
-                constexpr int i = decltype(tile)::value;
-                const uint32_t vd = v_lo + (vt % KV_STAGES) * (C::TILE >> 4);
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < BLK / 16; ++k)
-                        mma_ts(tmem + 256 + i * D, tmem + 128 * i + 8 * k, vd + ((k * 16 * 128) >> 4), id_o, k != 0 || !first);
-                }
             };
             auto commit = [&](uint32_t b) {
                 if (leader) tc::mma_commit(b);
             };
+            // `st` 0 / 1: the half of the ring (K tile 2 st, V tile 2 st + 1), a constant so that descriptors are too
+            auto scores = [&](auto tile, auto st) {
+                constexpr int i = decltype(tile)::value, o = 2 * decltype(st)::value * (C::TILE >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * C::HALF + (k % 4) * 32) >> 4;
+                        mma_ss(tmem + 128 * i, q_lo + i * (C::TILE >> 4) + off, k_lo + o + off, id_s, k != 0);
+                    }
+                    tc::mma_commit(sfull(i));
+                }
+            };
+            auto values = [&](auto tile, auto st, bool first) {
+                constexpr int i = decltype(tile)::value, o = (2 * decltype(st)::value + 1) * (C::TILE >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < BLK / 16; ++k)
+                        mma_ts(tmem + 256 + i * D, tmem + 128 * i + 8 * k, v_lo + o + ((k * 16 * 128) >> 4), id_o, k != 0 || !first);
+                }
+            };
             using T0 = std::integral_constant<int, 0>;
             using T1 = std::integral_constant<int, 1>;
+            // scores of an item's first block (block n of this CTA, in half `st` of the ring)
+            auto open = [&](auto st, bool two) {
+                constexpr int h = decltype(st)::value;
+                if (!wait(tfull(2 * h), (n >> 1) & 1) || !wait(qfull(0), nq0++ & 1)) return false;
+                scores(T0{}, st);
+                if (two) {
+                    if (!wait(qfull(1), nq1++ & 1)) return false;
+                    scores(T1{}, st);
+                }
+                commit(tempty(2 * h));
+                return true;
+            };
+            // values of block n, scores of block n + 1 if the piece has it: tile 0, then tile 1
+            auto step = [&](auto st, bool two, bool first, bool more) {
+                constexpr int h = decltype(st)::value;
+                using Next = std::integral_constant<int, 1 - h>;
+                if (!wait(tfull(2 * h + 1), (n >> 1) & 1)) return false;
+                if (more && !wait(tfull(2 * (1 - h)), ((n + 1) >> 1) & 1)) return false;
+                if (!wait(pfull(0), np0++ & 1)) return false;
+                values(T0{}, st, first);
+                if (more)
+                    scores(T0{}, Next{});
+                else
+                    commit(ofull(0));
+                if (two) {
+                    if (!wait(pfull(1), np1++ & 1)) return false;
+                    values(T1{}, st, first);
+                    if (!more) commit(ofull(1));
+                }
+                commit(tempty(2 * h + 1));
+                if (more) {
+                    if (two) scores(T1{}, Next{});
+                    commit(tempty(2 * (1 - h)));
+                }
+                ++n;
+                return true;
+            };
             while (ok && p.next(a, b0, b1)) {
                 const bool two = p.w.n_q * a.group - p.t * ROWS > TM;
-                const int cnt = b1 - b0;
-                // scores of the first block
-                uint32_t kt = 2 * n;
-                if (!wait(tfull(kt % KV_STAGES), (kt / KV_STAGES) & 1)) break;
-                if (!wait(qfull(0), nq0++ & 1)) break;
-                scores(T0{}, kt);
-                if (two) {
-                    if (!wait(qfull(1), nq1++ & 1)) break;
-                    scores(T1{}, kt);
-                }
-                commit(tempty(kt % KV_STAGES));
-                // values of block j, scores of block j + 1: tile 0, then tile 1
-                for (int j = 0; j < cnt; ++j, ++n) {
-                    const bool more = j + 1 < cnt;
-                    const uint32_t vt = 2 * n + 1;
-                    kt = 2 * n + 2;
-                    if (!wait(tfull(vt % KV_STAGES), (vt / KV_STAGES) & 1)) break;
-                    if (!wait(pfull(0), np0++ & 1)) break;
-                    values(T0{}, vt, j == 0);
-                    if (!more) commit(ofull(0));
-                    if (more) {
-                        if (!wait(tfull(kt % KV_STAGES), (kt / KV_STAGES) & 1)) break;
-                        scores(T0{}, kt);
-                    }
-                    if (two) {
-                        if (!wait(pfull(1), np1++ & 1)) break;
-                        values(T1{}, vt, j == 0);
-                        if (!more) commit(ofull(1));
-                    }
-                    commit(tempty(vt % KV_STAGES));
-                    if (more) {
-                        if (two) scores(T1{}, kt);
-                        commit(tempty(kt % KV_STAGES));
-                    }
-                }
+                if (!(n & 1 ? open(T1{}, two) : open(T0{}, two))) break;
+                for (int j = b0; j < b1; ++j)
+                    if (!(n & 1 ? step(T1{}, two, j == b0, j + 1 < b1) : step(T0{}, two, j == b0, j + 1 < b1))) break;
             }
             if (!ok && lane == 0) give_up();
             __syncwarp();
         }
-    } else if (warp >= 8) {
+    } else if (warp >= SOFT_WARPS) {
         // ---------------------------------------------------------------- unpack
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(UNPACK_REGS));
         // A lane owns the group `gr` of a key: four words and one step. The order in which lanes take the
         // octets makes both the word loads (32 lanes, 32 banks) and the 16-byte stores (8 lanes of a phase, 8
         // chunks of a 128-byte row) free of bank conflicts.
-        Pieces p = start_sh;
         constexpr int KPW = 32 / G;               // keys per warp and pass
-        constexpr int PASSES = BLK / (4 * KPW);
+        constexpr int KPP = UNPACK_WARPS * KPW;   // keys per pass
+        constexpr int PASSES = BLK / KPP;
         const int gr = lane % G;
-        const int row = (warp - 8) * KPW + lane / G;  // key of the first pass
+        const int row = (warp - SOFT_WARPS) * KPW + lane / G;  // key of the first pass
         int loads[4], stores[4];                  // byte offsets of the i-th octet, the same in every pass
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -493,54 +534,45 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             loads[i] = row * VB + 4 * (t * G + gr);
             stores[i] = (gr >> 1) * C::HALF + row * 128 + (((4 * (gr & 1) + t) ^ (row & 7)) << 4);
         }
-        uint32_t g = 0;
-        int b0, b1;
-        bool ok = true;
-        while (ok && p.next(a, b0, b1)) {
-            for (int b = b0; b < b1 && ok; ++b) {
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v, ++g) {
-                    const int cs = g % CODE_STAGES, ts = g % KV_STAGES;
-                    ok = !*aborted && tc::mbar_wait(cfull(cs), (g / CODE_STAGES) & 1, WAIT_NS) &&
-                         (g < KV_STAGES || tc::mbar_wait(tempty(ts), (g / KV_STAGES - 1) & 1, WAIT_NS));
-                    if (!ok) {
-                        give_up();
-                        break;
-                    }
-                    const uint8_t* codes = sC + cs * C::PACKED;
-                    uint8_t* tile = sT + ts * C::TILE;
-                    // all loads first: the compiler may not move one across a store to shared memory
-                    uint32_t word[PASSES][4], st[PASSES];
+        for (uint32_t g = 0;; ++g) {
+            const int cs = g % CODE_STAGES, ts = g % KV_STAGES;
+            if (*aborted || !tc::mbar_wait(cfull(cs), (g / CODE_STAGES) & 1, WAIT_NS) ||
+                (g >= KV_STAGES && valid_sh[cs] >= 0 && !tc::mbar_wait(tempty(ts), (g / KV_STAGES - 1) & 1, WAIT_NS))) {
+                give_up();
+                break;
+            }
+            const int valid = valid_sh[cs];
+            if (valid < 0) break;
+            const uint8_t* codes = sC + cs * C::PACKED;
+            uint8_t* tile = sT + ts * C::TILE;
+            // all loads first: the compiler may not move one across a store to shared memory
+            uint32_t word[PASSES][4], st[PASSES];
 #pragma unroll
-                    for (int pass = 0; pass < PASSES; ++pass) {
-                        st[pass] = *reinterpret_cast<const uint16_t*>(codes + C::CODES + (pass * 4 * KPW + row) * 2 * G + 2 * gr);
+            for (int pass = 0; pass < PASSES; ++pass) {
+                st[pass] = *reinterpret_cast<const uint16_t*>(codes + C::CODES + (pass * KPP + row) * 2 * G + 2 * gr);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            word[pass][i] = *reinterpret_cast<const uint32_t*>(codes + loads[i] + pass * 4 * KPW * VB);
-                    }
+                for (int i = 0; i < 4; ++i) word[pass][i] = *reinterpret_cast<const uint32_t*>(codes + loads[i] + pass * KPP * VB);
+            }
 #pragma unroll
-                    for (int pass = 0; pass < PASSES; ++pass) {
-                        // behind the last token: whatever the page holds
-                        if (b * BLK + pass * 4 * KPW + row >= p.w.len) st[pass] = 0;
-                        st[pass] = __byte_perm(st[pass], 0, 0x1010);
-                        const uint32_t s16 = bf16x2_mul(st[pass], kBf16x2Sixteen), s24 = bf16x2_mul(st[pass], kBf16x2MinusTwentyFour);
+            for (int pass = 0; pass < PASSES; ++pass) {
+                if (pass * KPP + row >= valid) st[pass] = 0;  // behind the last token: whatever the page holds
+                st[pass] = __byte_perm(st[pass], 0, 0x1010);
+                const uint32_t s16 = bf16x2_mul(st[pass], kBf16x2Sixteen), s24 = bf16x2_mul(st[pass], kBf16x2MinusTwentyFour);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t x = word[pass][i];
-                            *reinterpret_cast<uint4*>(tile + stores[i] + pass * 4 * KPW * 128) =
-                                make_uint4(bf16x2_fma(kv4_unit_pair<0>(x), s16, s24), bf16x2_fma(kv4_unit_pair<1>(x), s16, s24),
-                                           bf16x2_fma(kv4_unit_pair<2>(x), s16, s24), bf16x2_fma(kv4_unit_pair<3>(x), s16, s24));
-                        }
-                    }
-                    tc::mbar_arrive(cempty(cs));
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(tfull(ts));
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = word[pass][i];
+                    *reinterpret_cast<uint4*>(tile + stores[i] + pass * KPP * 128) =
+                        make_uint4(bf16x2_fma(kv4_unit_pair<0>(x), s16, s24), bf16x2_fma(kv4_unit_pair<1>(x), s16, s24),
+                                   bf16x2_fma(kv4_unit_pair<2>(x), s16, s24), bf16x2_fma(kv4_unit_pair<3>(x), s16, s24));
                 }
             }
+            tc::mbar_arrive(cempty(cs));
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(tfull(ts));
         }
     } else {
         // ---------------------------------------------------------------- softmax: tile i, row r of it
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFT_REGS));
         const int i = warp >> 2, r = tid & (TM - 1);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + 128 * i + lanes, tO = tmem + 256 + D * i + lanes;
@@ -582,83 +614,104 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             }
             return true;
         };
+        // 16 bytes `o8` of row `rr` of the tile's query memory
+        auto cell = [&](int rr, int o8) {
+            return reinterpret_cast<uint4*>(sQ + i * C::TILE + (o8 >> 3) * C::HALF + rr * 128 + (((o8 & 7) ^ (rr & 7)) << 4));
+        };
         bool ok = true;
         bool have = fetch();
         while (have) {
 #pragma unroll
             for (int x = 0; x < QN; ++x) {
-                const int rr = (warp & 3) * 32 + x * RPI + lane / LPR;
                 const uint4 v = qv[x];
-                *reinterpret_cast<uint4*>(sQ + i * C::TILE + (oct >> 3) * C::HALF + rr * 128 + (((oct & 7) ^ (rr & 7)) << 4)) =
+                *cell((warp & 3) * 32 + x * RPI + lane / LPR, oct) =
                     make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                                __byte_perm(v.y, v.w, 0x7632));
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(qfull(i));
-            float mx = -INFINITY, thr = -INFINITY, msc = 0.0f, den = 0.0f;
+            float mx = -INFINITY, msc = 0.0f, den = 0.0f;
             for (int b = b0; b < b1; ++b, ++ns) {
                 ok = !*aborted && tc::mbar_wait(sfull(i), ns & 1, WAIT_NS);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc::fence_after_sync();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc::tmem_ld_32x32(tS + 32 * k, s[k]);
-                tc::tmem_ld_wait();
-                if (b * BLK + BLK > least) {
-                    const int seen = limit - b * BLK;  // columns this row sees
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                const int seen = limit - b * BLK;  // columns this row sees
+                const bool masked = b * BLK + BLK > least;
+                uint32_t s[2][32];
+                auto load = [&](int k) { tc::tmem_ld_32x32(tS + 32 * k, s[k & 1]); };
+                auto mask = [&](int k) {
+                    if (masked) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
-                            if (32 * k + x >= seen) s[k][x] = 0xFF800000u;
-                }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int x = 0; x < 32; x += 2)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], __uint_as_float(s[k][x]), __uint_as_float(s[k][x + 1]));
-                const float m = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-                const bool raise = m > thr;
-                if (__any_sync(0xffffffffu, raise)) {
-                    float f = 1.0f;
-                    if (raise) {
-                        const float now = m * sc;
-                        f = mx == -INFINITY ? 0.0f : exp2_approx(msc - now);
-                        mx = m;
-                        msc = now;
-                        thr = m + RAISE / sc;
-                        den *= f;
+                            if (32 * k + x >= seen) s[k & 1][x] = 0xFF800000u;
                     }
-                    if (b > b0) {  // the block before has been added: its MMA finished before this S
-#pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tc::tmem_ld_32x32(tO + 32 * k, o);
-                            tc::tmem_ld_wait();
+                };
+                // Exponentials against the maximum so far. A row whose sum shows that its maximum has grown too much
+                // (always on the first block) has it raised, and the warp takes the pass again: the scores stay where
+                // they are until P is stored over them. Nothing else looks at the scores' maximum.
+                float sum = 0.0f;
+                uint32_t pk[2][32];
+                for (bool again = b == b0;;) {
+                    if (again) {
+                        float m = -INFINITY;
+                        load(0);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tc::tmem_st_32x32(tO + 32 * k, o);
+                        for (int k = 0; k < 4; ++k) {
+                            tc::tmem_ld_wait();
+                            if (k < 3) load(k + 1);
+                            mask(k);
+#pragma unroll
+                            for (int x = 0; x < 32; x += 2)
+                                m = max3(m, __uint_as_float(s[k & 1][x]), __uint_as_float(s[k & 1][x + 1]));
+                        }
+                        float f = 1.0f;
+                        if (m > mx) {
+                            const float now = m * sc;
+                            f = mx == -INFINITY ? 0.0f : exp2_approx(msc - now);
+                            mx = m;
+                            msc = now;
+                            den *= f;
+                        }
+                        if (b > b0) {  // the block before has been added: its MMA finished before this S
+#pragma unroll 1
+                            for (int k = 0; k < D / 32; ++k) {
+                                tc::tmem_ld_32x32(tO + 32 * k, s[0]);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[0][x] = __float_as_uint(__uint_as_float(s[0][x]) * f);
+                                tc::tmem_st_32x32(tO + 32 * k, s[0]);
+                            }
                         }
                     }
-                }
-                const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-msc, -msc);
-                float2 d2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-msc, -msc);
+                    float2 d2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    load(0);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
+                    for (int k = 0; k < 4; ++k) {
+                        tc::tmem_ld_wait();
+                        if (k < 3) load(k + 1);
+                        mask(k);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const int k = 2 * h + (x >> 4), y = 2 * (x & 15);
-                        float2 e = fma2(make_float2(__uint_as_float(s[k][y]), __uint_as_float(s[k][y + 1])), sc2, off2);
-                        e.x = exp2_approx(e.x);
-                        e.y = exp2_approx(e.y);
-                        d2[x & 1] = add2(d2[x & 1], e);
-                        pk[x] = pack_bf16(e.x, e.y);
+                        for (int x = 0; x < 16; ++x) {
+                            float2 e = fma2(make_float2(__uint_as_float(s[k & 1][2 * x]), __uint_as_float(s[k & 1][2 * x + 1])), sc2, off2);
+                            if (POLY_EVERY && x % (POLY_EVERY + !POLY_EVERY) == POLY_EVERY - 1) {
+                                e = exp2_poly(e);
+                            } else {
+                                e.x = exp2_approx(e.x);
+                                e.y = exp2_approx(e.y);
+                            }
+                            d2[x & 1] = add2(d2[x & 1], e);
+                            pk[k >> 1][16 * (k & 1) + x] = pack_bf16(e.x, e.y);
+                        }
                     }
-                    tc::tmem_st_32x32(tS + 32 * h, pk);
+                    sum = (d2[0].x + d2[0].y) + (d2[1].x + d2[1].y);
+                    if (again || !__any_sync(0xffffffffu, sum > RAISE_SUM)) break;
+                    again = true;
                 }
-                den += (d2[0].x + d2[0].y) + (d2[1].x + d2[1].y);
+                tc::tmem_st_32x32(tS, pk[0]);
+                tc::tmem_st_32x32(tS + 32, pk[1]);
+                den += sum;
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 tc::mbar_arrive(pfull(i));
@@ -681,7 +734,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
             float4* slot = reinterpret_cast<float4*>(a.slots + slot_at) + i * TM + r;
             // whole rows go out through the tile's query memory, which no MMA reads any more
-            uint8_t* stage = sQ + i * C::TILE;
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
@@ -695,29 +747,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         f[j] = __uint_as_float(o[x + 2 * j]);
                         f[j + 4] = __uint_as_float(o[x + 2 * j + 1]);
                     }
+                    const int o8 = 4 * k + x / 8;  // octet of dims
                     if (whole) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) f[j] *= inv;
-                        const int o8 = 4 * k + x / 8;
-                        *reinterpret_cast<uint4*>(stage + (o8 >> 3) * C::HALF + r * 128 + (((o8 & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                        *cell(r, o8) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
                     } else {
-                        slot[(8 * k + x / 4) * ROWS] = make_float4(f[0], f[1], f[2], f[3]);
-                        slot[(8 * k + x / 4 + 1) * ROWS] = make_float4(f[4], f[5], f[6], f[7]);
+                        slot[2 * o8 * ROWS] = make_float4(f[0], f[1], f[2], f[3]);
+                        slot[(2 * o8 + 1) * ROWS] = make_float4(f[4], f[5], f[6], f[7]);
                     }
                 }
             }
             if (whole) {
                 __syncwarp();
 #pragma unroll 4
-                for (int x = 0; x < 32 / RPI; ++x) {
-                    const int from = x * RPI + lane / LPR, rr = (warp & 3) * 32 + from;
+                for (int x = 0; x < QN; ++x) {
+                    const int from = x * RPI + lane / LPR;
                     const int64_t off = __shfl_sync(0xffffffffu, row, from);
-                    if (off >= 0)
-                        *reinterpret_cast<uint4*>(a.out + off + 8 * oct) =
-                            *reinterpret_cast<const uint4*>(stage + (oct >> 3) * C::HALF + rr * 128 + (((oct & 7) ^ (rr & 7)) << 4));
+                    if (off >= 0) *reinterpret_cast<uint4*>(a.out + off + 8 * oct) = *cell((warp & 3) * 32 + from, oct);
                 }
-                __syncwarp();  // before the next item's queries overwrite the rows
+                __syncwarp();  // the warp's own next queries go to the rows that it has just read
             } else {
                 float2* st = reinterpret_cast<float2*>(a.slots + slot_at + ROWS * D) + i * TM + r;
                 *st = make_float2(mx == -INFINITY ? -INFINITY : msc, den);
@@ -729,7 +778,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     // -------------------------------------------------------------------- teardown
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == MMA_WARP) {
         if (abort_sh) {
             // no MMA may still be using TMEM when it is released
             if (elect_one()) tc::mma_commit(drained);
