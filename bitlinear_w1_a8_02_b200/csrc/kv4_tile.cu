@@ -46,7 +46,7 @@ constexpr int THREADS = 32 * (LOAD_WARP + 4);
 constexpr int LAUNCH_REGS = 96, SOFT_REGS = 160, UNPACK_REGS = 48, REST_REGS = 56;
 static_assert(2 * SOFT_REGS + 2 * UNPACK_REGS + REST_REGS <= 5 * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536, "register split");
 constexpr int MAX_CTAS = 148;     // sizes the workspace
-constexpr int ITEM_UNITS = 2;     // what starting and ending an item costs, in units (it evens out the ranges)
+constexpr int ITEM_UNITS = 4;     // what starting and ending an item costs, in units (it evens out the ranges)
 constexpr int SEQ_GROUP = 32;     // sequences per entry of the coarse unit table
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr float RAISE_SUM = 1024.0f;  // sum of a row's exponentials over a block that raises its maximum
@@ -58,6 +58,7 @@ struct TileArgs {
     Kv4View cache;
     Kv4Seqs batch;
     int M, group, max_q;
+    uint64_t group_inv;  // ceil(2^40 / group): rows / group as a multiplication
     float scale_log2;
     float* slots;   // [2 gridDim.x] pieces: [D / 4][ROWS] float4 sums, then [ROWS] (maximum, denominator)
     int4* joins;    // [gridDim.x]
@@ -159,7 +160,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // |f| <= 1/2, by adding 1.5 * 2^23; 2^f by a cubic (fitted to the least largest
 // relative error, 7.5e-05, a fraction of a bf16 rounding); 2^n as an exponent.
 // x below -127 gives 0, a NaN stays one.
-constexpr int POLY_EVERY = 0;
+constexpr int POLY_EVERY = 4;
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
@@ -195,15 +196,47 @@ __device__ __forceinline__ Seq seq_of(const TileArgs& a, int s, bool report) {
     return w;
 }
 
+// n / group for 0 <= n < 2^29 (group <= 1024): exact, since n * group < 2^40.
+__device__ __forceinline__ int per_group(const TileArgs& a, int n) { return (int)(((uint64_t)n * a.group_inv) >> 40); }
+
 // Blocks of item t of a sequence: up to the last key that its last row sees.
 __device__ __forceinline__ int blocks_of(const TileArgs& a, const Seq& w, int t) {
-    const int last = min(w.n_q - 1, ((t + 1) * ROWS - 1) / a.group);
+    const int last = min(w.n_q - 1, per_group(a, (t + 1) * ROWS - 1));
     return max(1, (w.len - w.n_q + last + 1 + BLK - 1) / BLK);
 }
 
-__device__ __forceinline__ int units_of(const TileArgs& a, const Seq& w) {
-    int n = w.tiles * ITEM_UNITS;
-    for (int t = 0; t < w.tiles; ++t) n += blocks_of(a, w, t);
+__device__ __forceinline__ int warp_scan(int v) {  // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+// Units of the SEQ_GROUP sequences of group g, sequence g * SEQ_GROUP + lane in each lane; the warp shares the
+// tiles of each long sequence.
+__device__ __forceinline__ int group_units(const TileArgs& a, int g, bool report) {
+    const int lane = threadIdx.x & 31, s = g * SEQ_GROUP + lane;
+    Seq w;
+    w.row0 = w.n_q = w.len = w.tiles = 0;
+    if (s < a.batch.S) w = seq_of(a, s, report);
+    int n = 0;
+    if (w.tiles <= 2) {
+        for (int t = 0; t < w.tiles; ++t) n += ITEM_UNITS + blocks_of(a, w, t);
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, w.tiles > 2); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        Seq x;
+        x.n_q = __shfl_sync(0xffffffffu, w.n_q, from);
+        x.len = __shfl_sync(0xffffffffu, w.len, from);
+        x.tiles = __shfl_sync(0xffffffffu, w.tiles, from);
+        int sum = 0;
+        for (int t = lane; t < x.tiles; t += 32) sum += ITEM_UNITS + blocks_of(a, x, t);
+        sum = warp_sum(sum);
+        if (lane == from) n = sum;
+    }
     return n * a.cache.hkv;
 }
 
@@ -249,8 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     __shared__ uint64_t bars[2 * KV_STAGES + 2 * CODE_STAGES + 9];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
-    __shared__ int warp_sums[THREADS / 32];
-    __shared__ int coarse[kKv4MaxSeqs / SEQ_GROUP + 1];  // units before each group of sequences
+    __shared__ int coarse[kKv4MaxSeqs / SEQ_GROUP + 1];  // [g + 1]: units up to the end of group g of sequences
     __shared__ Pieces start_sh;
     __shared__ int total_sh;
     __shared__ int valid_sh[CODE_STAGES];  // keys of a packed tile, -1 after the last
@@ -288,53 +320,55 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // ---- units of all sequences, and this CTA's range of them
-    const int S = a.batch.S;
-    {
+    // ---- units of all sequences, and where this CTA's range of them starts
+    const int groups = (a.batch.S + SEQ_GROUP - 1) / SEQ_GROUP;
+    for (int g = warp; g < groups; g += THREADS / 32) {
+        const int sum = warp_sum(group_units(a, g, blockIdx.x == 0));
+        if (lane == 0) coarse[g + 1] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
         int carry = 0;
-        for (int s0 = 0; s0 < S; s0 += THREADS) {
-            const int s = s0 + tid;
-            const int u = s < S ? units_of(a, seq_of(a, s, blockIdx.x == 0)) : 0;
-            int sum = u;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) warp_sums[warp] = sum;
-            __syncthreads();
-            if (tid == 0)
-                for (int w = 0; w < THREADS / 32 && s0 + w * SEQ_GROUP < S; ++w) {
-                    coarse[s0 / SEQ_GROUP + w] = carry;
-                    carry += warp_sums[w];
-                }
-            __syncthreads();
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane;
+            const int sum = carry + warp_scan(g < groups ? coarse[g + 1] : 0);
+            if (g < groups) coarse[g + 1] = sum;
+            carry = __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (tid == 0) {
-            coarse[(S + SEQ_GROUP - 1) / SEQ_GROUP] = carry;
-            total_sh = carry;
-            const int ctas = min((int)gridDim.x, carry);
-            if ((int)blockIdx.x < ctas) {
-                Pieces p;
-                p.u = (int)((long long)carry * blockIdx.x / ctas);
-                p.u1 = (int)((long long)carry * (blockIdx.x + 1) / ctas);
-                int g = 0;
-                while (coarse[g + 1] <= p.u) ++g;
-                int before = coarse[g];
-                for (p.s = g * SEQ_GROUP;; ++p.s) {
-                    p.w = seq_of(a, p.s, false);
-                    const int n = units_of(a, p.w);
-                    if (before + n > p.u) break;
-                    before += n;
+        __syncwarp();
+        const int ctas = min((int)gridDim.x, carry);
+        if ((int)blockIdx.x < ctas) {
+            Pieces p;
+            p.u = (int)((long long)carry * blockIdx.x / ctas);
+            p.u1 = (int)((long long)carry * (blockIdx.x + 1) / ctas);
+            int g = 0;  // the group that holds u: the number of groups that end at or before it
+            for (int g0 = 0; g0 < groups; g0 += 32)
+                g += __popc(__ballot_sync(0xffffffffu, g0 + lane < groups && coarse[g0 + lane + 1] <= p.u));
+            const int n = group_units(a, g, false);
+            const int before = g ? coarse[g] : 0;
+            const int upto = before + warp_scan(n);
+            const int in = __popc(__ballot_sync(0xffffffffu, upto <= p.u));  // < 32: the group holds u
+            p.s = g * SEQ_GROUP + in;
+            p.w = seq_of(a, p.s, false);
+            int at = __shfl_sync(0xffffffffu, upto - n, in);  // units before the sequence
+            for (int t0 = 0;; t0 += 32) {
+                const int t = t0 + lane;
+                const int b = t < p.w.tiles ? (ITEM_UNITS + blocks_of(a, p.w, t)) * a.cache.hkv : 0;
+                const int end = at + warp_scan(b);
+                const int k = __popc(__ballot_sync(0xffffffffu, t < p.w.tiles && end <= p.u));
+                if (k < 32) {
+                    p.t = t0 + k;
+                    at = __shfl_sync(0xffffffffu, end - b, k);
+                    break;
                 }
-                for (p.t = 0;; ++p.t) {
-                    p.blocks = blocks_of(a, p.w, p.t);
-                    const int n = (ITEM_UNITS + p.blocks) * a.cache.hkv;
-                    if (before + n > p.u) break;
-                    before += n;
-                }
-                p.head = (p.u - before) / (ITEM_UNITS + p.blocks);
-                p.first = before + p.head * (ITEM_UNITS + p.blocks);
-                start_sh = p;
+                at = __shfl_sync(0xffffffffu, end, 31);
             }
+            p.blocks = blocks_of(a, p.w, p.t);
+            p.head = (p.u - at) / (ITEM_UNITS + p.blocks);
+            p.first = at + p.head * (ITEM_UNITS + p.blocks);
+            if (lane == 0) start_sh = p;
         }
+        if (lane == 0) total_sh = carry;
     }
     __syncthreads();
     const int total = total_sh;
@@ -582,12 +616,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
         int4 join = make_int4(0, 0, 0, -1);
         constexpr int LPR = D / 8, RPI = 32 / LPR, QN = 32 / RPI;  // lanes of a row, rows and count of 16-byte accesses
         const int oct = lane % LPR;
-        // The next piece that has rows in this tile: what the thread needs to know of it, and the warp's 32 rows of
-        // queries on their way into registers, D / 8 lanes to a row.
+        // The next piece that has rows in this tile: what the thread needs to know of it. Its queries start on their
+        // way to L2; they are loaded once the tile's memory is free.
         int b0 = 0, b1 = 0, limit = 0, least = 0;
-        int64_t row_out = -1;  // this row's offset in out, -1 for a row that does not exist
+        int64_t row_out = -1, row_q = -1;  // this row's offsets in out and q, -1 for a row that does not exist
         bool starts = false, ends = false;
-        uint4 qv[QN];
         auto fetch = [&]() {
             int rows;
             do {
@@ -601,16 +634,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             } while (i * TM >= rows);
             const bool live = i * TM + r < rows;
             const int ri = p.t * ROWS + i * TM + r;  // row of the sequence
-            const int token = ri / a.group, qh = p.head * a.group + ri % a.group;
+            const int token = per_group(a, ri), qh = p.head * a.group + ri - token * a.group;
             limit = live ? min(p.w.len, p.w.len - p.w.n_q + token + 1) : 0;
-            least = p.w.len - p.w.n_q + (p.t * ROWS + i * TM) / a.group + 1;  // keys all rows see
+            least = p.w.len - p.w.n_q + per_group(a, p.t * ROWS + i * TM) + 1;  // keys all rows see
             row_out = live ? (int64_t)(p.w.row0 + token) * a.out_stride + qh * D : -1;
-            const int64_t qoff = live ? (int64_t)(p.w.row0 + token) * a.q_stride + qh * D : -1;
+            row_q = live ? (int64_t)(p.w.row0 + token) * a.q_stride + qh * D : -1;
+            if (live) {
 #pragma unroll
-            for (int x = 0; x < QN; ++x) {
-                const int64_t off = __shfl_sync(0xffffffffu, qoff, x * RPI + lane / LPR);
-                qv[x] = make_uint4(0, 0, 0, 0);
-                if (off >= 0) qv[x] = *reinterpret_cast<const uint4*>(a.q + off + 8 * oct);
+                for (int x = 0; x < D; x += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row_q + x));
             }
             return true;
         };
@@ -621,12 +652,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
         bool ok = true;
         bool have = fetch();
         while (have) {
+            // the warp's 32 rows of queries, D / 8 lanes to a row
+#pragma unroll 1
+            for (int x0 = 0; x0 < QN; x0 += QN / 2) {
+                uint4 v[QN / 2];
 #pragma unroll
-            for (int x = 0; x < QN; ++x) {
-                const uint4 v = qv[x];
-                *cell((warp & 3) * 32 + x * RPI + lane / LPR, oct) =
-                    make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                               __byte_perm(v.y, v.w, 0x7632));
+                for (int x = 0; x < QN / 2; ++x) {
+                    const int64_t off = __shfl_sync(0xffffffffu, row_q, (x0 + x) * RPI + lane / LPR);
+                    v[x] = make_uint4(0, 0, 0, 0);
+                    if (off >= 0) v[x] = *reinterpret_cast<const uint4*>(a.q + off + 8 * oct);
+                }
+#pragma unroll
+                for (int x = 0; x < QN / 2; ++x)
+                    *cell((warp & 3) * 32 + (x0 + x) * RPI + lane / LPR, oct) =
+                        make_uint4(__byte_perm(v[x].x, v[x].z, 0x5410), __byte_perm(v[x].x, v[x].z, 0x7632),
+                                   __byte_perm(v[x].y, v[x].w, 0x5410), __byte_perm(v[x].y, v[x].w, 0x7632));
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(qfull(i));
@@ -716,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 tc::fence_before_sync();
                 tc::mbar_arrive(pfull(i));
             }
-            // this piece's rows, before the next piece's take their place; its queries load during the last product
+            // this piece's rows, before the next piece's take their place
             const bool whole = starts && ends;
             const int64_t row = row_out;
             const size_t slot_at = (size_t)(2 * c + (starts ? 1 : 0)) * C::SLOT;
@@ -734,11 +774,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             const float inv = den == 0.0f ? 0.0f : 1.0f / den;
             float4* slot = reinterpret_cast<float4*>(a.slots + slot_at) + i * TM + r;
             // whole rows go out through the tile's query memory, which no MMA reads any more
-#pragma unroll 1
+            uint32_t ov[2][32];
+            tc::tmem_ld_32x32(tO, ov[0]);
+#pragma unroll
             for (int k = 0; k < D / 32; ++k) {
-                uint32_t o[32];
-                tc::tmem_ld_32x32(tO + 32 * k, o);
+                uint32_t(&o)[32] = ov[k & 1];
                 tc::tmem_ld_wait();
+                if (k + 1 < D / 32) tc::tmem_ld_32x32(tO + 32 * (k + 1), ov[(k + 1) & 1]);
 #pragma unroll
                 for (int x = 0; x < 32; x += 8) {
                     float f[8];  // back in order: column 2j is dim j, column 2j + 1 dim j + 4
@@ -863,6 +905,7 @@ cudaError_t launch_kv4_tile(const uint16_t* q, int64_t q_stride, int64_t M, int 
     a.q = q, a.out = out, a.q_stride = q_stride, a.out_stride = out_stride;
     a.cache = cache, a.batch = batch;
     a.M = (int)M, a.group = Hq / cache.hkv, a.max_q = (int)std::min<int64_t>(max_q, M);
+    a.group_inv = (((uint64_t)1 << 40) + a.group - 1) / a.group;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.slots = (float*)ws;
     a.joins = (int4*)((char*)ws + (size_t)2 * MAX_CTAS * ROWS * (D + 2) * 4);
