@@ -18,11 +18,11 @@
 // A running maximum is kept per row and only raised when a score passes it by
 // 2^8 (in the exponent's base-2 units), so accumulators are rarely rescaled.
 //
-// Work split: all (sequence, head, row block) items are cut into units of 64
+// Work split: all (sequence, head, row block) items are cut into units of 128
 // keys and every CTA takes one contiguous range of units, whatever the lengths
 // are. A CTA that holds a whole item writes its rows; a piece goes to the CTA's
 // slot in the workspace as unnormalised sums, maximum and denominator, and a
-// second kernel joins the pieces in order. Four warps take 16 keys of a unit
+// second kernel joins the pieces in order. Four warps take 32 keys of a unit
 // each; a fifth copies the units' pages into a ring (bulk copies, the page ids
 // of 32 copies ahead loaded at once).
 #include <algorithm>
@@ -33,10 +33,11 @@
 namespace bl {
 namespace {
 
-constexpr int kKeys = 64;        // keys per unit
-constexpr int kWarps = 4;        // consumer warps, 16 keys of a unit each
+constexpr int kKeys = 128;       // keys per unit
+constexpr int kWarps = 4;        // consumer warps, 32 keys of a unit each, 16 at a time
+constexpr int kWarpKeys = kKeys / kWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 constexpr int kMaxCtas = 592;    // four per SM on 148 SMs; sizes the workspace
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRaise = 8.0f;   // a maximum is raised when a score passes it by this (base 2)
@@ -84,6 +85,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with an accumulator operand of its own: rows r and r + 8 both start from (c0, c1).
+__device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -108,7 +118,7 @@ __device__ __forceinline__ uint32_t raw_pair(uint32_t w) {  // nibbles I, I + 4 
     return ((I == 0 ? w : w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
 }
 
-// Units of 64 keys of sequence s (0 when it has no new tokens or was refused).
+// Units of kKeys keys of sequence s (0 when it has no new tokens or was refused).
 struct SeqWork {
     int n_q, len, row0, blocks, row_blocks;
 };
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 
         // queries of this lane's rows (columns r of each n-tile) in the order of the nibbles, and -136 sum q
         uint32_t qf[NT][G][4];
-        float c0[NT][G][2];
+        float c0[NT][G][4];
         int lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -322,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 c0[nt][gr][0] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t);
                 c0[nt][gr][1] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                c0[nt][gr][2] = c0[nt][gr][0], c0[nt][gr][3] = c0[nt][gr][1];
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -349,11 +360,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             ok = tc::mbar_wait(full(st), (g / kStages) & 1, kWaitLimitNs) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const uint8_t* kc = ring + st * St::BYTES + warp * 16 * VB;
+#pragma unroll 1
+            for (int sub = 0; sub < kWarpKeys / 16; ++sub) {
+            const int at = warp * kWarpKeys + sub * 16;  // first of 16 keys
+            const int key0 = (u - it.first) * kKeys + at;
+            if (key0 >= it.w.len) break;  // behind the last token
+            const uint8_t* kc = ring + st * St::BYTES + at * VB;
             const uint8_t* vc = kc + St::CODES;
-            const uint16_t* ks = reinterpret_cast<const uint16_t*>(ring + st * St::BYTES + 2 * St::CODES) + warp * 16 * G;
+            const uint16_t* ks = reinterpret_cast<const uint16_t*>(ring + st * St::BYTES + 2 * St::CODES) + at * G;
             const uint16_t* vs = ks + St::STEPS / 2;
-            const int key0 = (u - it.first) * kKeys + warp * 16;
 
             // ---- scores of keys key0 + r and key0 + r + 8
             uint32_t ka[G], kb[G];
@@ -388,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 const uint32_t b0 = raw_pair<2>(ka[gr]), b1 = raw_pair<2>(kb[gr]), b2 = raw_pair<3>(ka[gr]), b3 = raw_pair<3>(kb[gr]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float d[4] = {c0[nt][gr][0], c0[nt][gr][1], c0[nt][gr][0], c0[nt][gr][1]};
-                    mma_bf16(d, a0, a1, a2, a3, qf[nt][gr][0], qf[nt][gr][1]);
+                    float d[4];
+                    mma_bf16_from(d, a0, a1, a2, a3, qf[nt][gr][0], qf[nt][gr][1], c0[nt][gr]);
                     mma_bf16(d, b0, b1, b2, b3, qf[nt][gr][2], qf[nt][gr][3]);
                     sv[nt][0] = fmaf(d[0], sa[gr], sv[nt][0]);
                     sv[nt][1] = fmaf(d[1], sa[gr], sv[nt][1]);
@@ -486,9 +501,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                     xw[kp][0][1] = __byte_perm(x, y, 0x7632);
                 }
             }
-            // everything this warp needs of the stage is in registers
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(empty(st));
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 // D = 128: rows r / r + 8 of tile i are nibble i of the lane's first / second word;
@@ -506,6 +518,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][i], f[0], f[1], f[2], f[3], pf[nt][0], pf[nt][1]);
             }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty(st));
         }
         if (!ok) {
             if (lane == 0) {
