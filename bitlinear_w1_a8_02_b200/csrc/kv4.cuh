@@ -55,11 +55,19 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return d;
 }
 
+// (a & b) | c as one instruction. With two immediates the compiler makes two of it; the constants are passed as
+// registers so that it does not.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 // Nibbles i (low half) and i + 4 (high half) of `w` as the bf16 pair 1 + n/16.
 template <int I>
 __device__ __forceinline__ uint32_t kv4_unit_pair(uint32_t w) {
     const uint32_t sh = I == 0 ? w << 3 : w >> (4 * I - 3);
-    return (sh & 0x00780078u) | 0x3F803F80u;
+    return and_or(sh, 0x00780078u, 0x3F803F80u);
 }
 
 constexpr uint32_t kBf16x2Sixteen = 0x41804180u;    // (16, 16)

@@ -37,6 +37,7 @@ constexpr int kKeys = 128;       // keys per unit
 constexpr int kWarps = 4;        // consumer warps, 32 keys of a unit each, 16 at a time
 constexpr int kWarpKeys = kKeys / kWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kItemUnits = 2;   // what starting and ending an item costs, in units (it evens out the ranges)
 constexpr int kStages = 2;
 constexpr int kMaxCtas = 592;    // four per SM on 148 SMs; sizes the workspace
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -77,6 +78,22 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// tc::mbar_wait with a hint that lets the warp sleep up to 20 us at a time: the polls of waiting warps take issue
+// slots from the unpacking ones.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    do {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    } while (tc::globaltimer_ns() - t0 <= kWaitLimitNs);
+    return false;
+}
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -115,7 +132,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 template <int I>
 __device__ __forceinline__ uint32_t raw_pair(uint32_t w) {  // nibbles I, I + 4 as 128 + n
-    return ((I == 0 ? w : w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
+    return and_or(I == 0 ? w : w >> (4 * I), 0x000F000Fu, 0x43004300u);
 }
 
 // Units of kKeys keys of sequence s (0 when it has no new tokens or was refused).
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         int u = 0;
         if (s < S) {
             const SeqWork w = seq_work<RB>(a, s, blockIdx.x == 0);
-            u = hkv * w.row_blocks * w.blocks;
+            u = hkv * w.row_blocks * (kItemUnits + w.blocks);
         }
         int sum = u;  // inclusive over the warp
 #pragma unroll
@@ -211,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 
     // The item that holds unit u: sequence by binary search, then head and row block.
     struct Item {
-        int s, head, rb, first;  // first: its first unit
+        int s, head, rb, first, end;  // units of its blocks; those that stand for its cost come before
         SeqWork w;
     };
     auto find = [&](int u) {
@@ -226,10 +243,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         Item it;
         it.s = lo;
         it.w = seq_work<RB>(a, lo, false);
-        const int j = (u - prefix[lo]) / it.w.blocks;
+        const int span = kItemUnits + it.w.blocks;
+        const int j = (u - prefix[lo]) / span;
         it.rb = j % it.w.row_blocks;
         it.head = j / it.w.row_blocks;
-        it.first = prefix[lo] + j * it.w.blocks;
+        it.first = prefix[lo] + j * span + kItemUnits;
+        it.end = it.first + it.w.blocks;
         return it;
     };
 
@@ -242,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         bool ok = true;
         for (int u = u0; u < u1 && ok;) {
             const Item it = find(u);
-            const int end = min(u1, it.first + it.w.blocks);
+            const int end = min(u1, it.end);
+            u = max(u, it.first);  // not past u1 by more than the item's cost: then there is no block here
             const int* row = a.batch.table + it.s * a.batch.table_stride;
             // page of part p (32 parts ahead, one per lane)
             int have = -1, page = 0;
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                         }
                     }
                 }
-                if (g >= kStages) ok = tc::mbar_wait(empty(st), (g / kStages - 1) & 1, kWaitLimitNs);
+                if (g >= kStages) ok = mbar_wait_asleep(empty(st), (g / kStages - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok && !*abort_flag);
                 if (!ok) break;
                 const int live = min(parts, (it.w.len - blk * kKeys + part_keys - 1) / part_keys);
@@ -301,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
     int4 join = make_int4(0, 0, 0, -1);
     for (int u = u0; u < u1;) {
         const Item it = find(u);
-        const int item_end = it.first + it.w.blocks;
-        const int end = min(u1, item_end);
+        const int end = min(u1, it.end);
+        u = max(u, it.first);
+        if (u >= end) continue;  // the range ends inside the item's cost
         const int rows = min(RB, it.w.n_q * a.group - it.rb * RB);
         const int begin = u;
 
@@ -357,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         bool ok = true;
         for (; u < end; ++u, ++g) {
             const int st = g % kStages;
-            ok = tc::mbar_wait(full(st), (g / kStages) & 1, kWaitLimitNs) && !*abort_flag;
+            ok = mbar_wait_asleep(full(st), (g / kStages) & 1) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
 #pragma unroll 1
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
         if (*abort_flag) break;  // the same for the four warps: set before the barrier, and nothing sets it after
-        const bool starts = begin == it.first, ends = end == item_end;
+        const bool starts = begin == it.first, ends = end == it.end;
         const bool whole = starts && ends;
         float* slot = a.slots + (size_t)(2 * c + (starts ? 1 : 0)) * RB * (D + 2);
         for (int x = tid; x < rows * (D / 4); x += 32 * kWarps) {
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         }
         if (starts && !ends) {
             // this CTA holds the item's first piece: the last one is with the CTA of its last unit
-            const int last = (int)(((long long)item_end * ctas + total - 1) / total) - 1;
+            const int last = (int)(((long long)it.end * ctas + total - 1) / total) - 1;
             join = make_int4(it.w.row0, it.head, it.rb | (rows << 24), last);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
@@ -603,35 +624,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
     if (tid == 0) a.joins[c] = join;
 }
 
-// Join the pieces of split items: block (c, row) takes row `row` of the item
-// whose first piece CTA c held: slot 2c + 1, then slot 2c' of the CTAs c' up to
-// the one that held its last unit, in order.
+// Join the pieces of split items: block c takes the item whose first piece CTA c
+// held: slot 2c + 1, then slot 2c' of the CTAs c' up to the one that held its last
+// unit, in order. A warp takes a row: its lanes first read the pieces' maxima and
+// denominators, 32 at a time, then the sums, 16 bytes each (D = 64: two pieces at
+// once), several pieces in flight.
 template <int D, int RB>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(32 * RB) kv4_join_kernel(const RowsArgs a) {
+    constexpr int VL = D / 4;        // lanes of a row
+    constexpr int PP = 32 / VL;      // pieces at once
     grid_dependency_wait();
     grid_dependents_launch();
     const int4 j = a.joins[blockIdx.x];
-    const int c = blockIdx.x, row = blockIdx.y, d = threadIdx.x;
+    const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (j.w < 0 || row >= (j.z >> 24)) return;
     const int pieces = j.w - c + 1;
     auto slot = [&](int p) { return a.slots + ((size_t)(2 * (c + p) + (p == 0 ? 1 : 0)) * RB + row) * (D + 2); };
     float m = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < pieces; ++p) m = fmaxf(m, slot(p)[D]);
-    float v = 0.0f, den = 0.0f;
-#pragma unroll 4
-    for (int p = 0; p < pieces; ++p) {
-        const float* sp = slot(p);
-        const float mp = sp[D], dp = sp[D + 1];
-        const float f = mp == -INFINITY ? (dp != dp ? 1.0f : 0.0f) : exp2_approx(mp - m);
-        den += f * dp;
-        v += f * sp[d];
+    for (int p = lane; p < pieces; p += 32) m = fmaxf(m, slot(p)[D]);
+    m = warp_max(m);
+    float den = 0.0f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int sub = lane / VL, d4 = 4 * (lane % VL);
+    for (int p0 = 0; p0 < pieces; p0 += 32) {
+        float f = 0.0f, d = 0.0f;
+        if (p0 + lane < pieces) {
+            const float2 st = *reinterpret_cast<const float2*>(slot(p0 + lane) + D);
+            f = st.x == -INFINITY ? (st.y != st.y ? 1.0f : 0.0f) : exp2_approx(st.x - m);
+            d = f * st.y;
+        }
+        den += warp_sum(d);
+        const int n = min(32, pieces - p0);
+#pragma unroll 8
+        for (int q = 0; q < n; q += PP) {
+            const float g = __shfl_sync(0xffffffffu, f, q + sub);
+            if (q + sub < n) {
+                const float* sp = slot(p0 + q + sub) + d4;  // 8-byte aligned
+                const float2 x = *reinterpret_cast<const float2*>(sp), y = *reinterpret_cast<const float2*>(sp + 2);
+                v.x += g * x.x, v.y += g * x.y, v.z += g * y.x, v.w += g * y.y;
+            }
+        }
     }
-    const float o = den == 0.0f ? 0.0f : v / den;
-    const int rb = j.z & 0xffffff;
-    const int ri = rb * RB + row;
-    const int token = j.x + ri / a.group;
-    a.out[(int64_t)token * a.out_stride + (j.y * a.group + ri % a.group) * D + d] = f32_to_bf16_bits(o);
+    if (PP == 2) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+    }
+    if (sub != 0) return;
+    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+    const int ri = (j.z & 0xffffff) * RB + row;
+    *reinterpret_cast<uint2*>(a.out + (int64_t)(j.x + ri / a.group) * a.out_stride + (j.y * a.group + ri % a.group) * D + d4) =
+        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
 template <int D, int NT>
@@ -654,7 +696,7 @@ cudaError_t launch_rows(const RowsArgs& args, int ctas_cap, cudaStream_t s) {
     const int grid = min(ctas_cap, dev < 64 ? resident[dev] : 148);
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, args);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv4_join_kernel<D, 8 * NT>, dim3((unsigned)grid, 8 * NT), dim3(D), 0, s, args);
+    return launch_pdl(kv4_join_kernel<D, 8 * NT>, dim3((unsigned)grid), dim3(32 * 8 * NT), 0, s, args);
 }
 
 }  // namespace
