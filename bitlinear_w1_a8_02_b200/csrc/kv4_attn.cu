@@ -96,8 +96,7 @@ __device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) 
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -105,8 +104,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // The same with an accumulator operand of its own: rows r and r + 8 both start from (c0, c1).
 __device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1, const float (&c)[4]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
@@ -381,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             ok = mbar_wait_asleep(full(st), (g / kStages) & 1) && !*abort_flag;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-#pragma unroll 1
+#pragma unroll
             for (int sub = 0; sub < kWarpKeys / 16; ++sub) {
             const int at = warp * kWarpKeys + sub * 16;  // first of 16 keys
             const int key0 = (u - it.first) * kKeys + at;
@@ -627,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 // Join the pieces of split items: block c takes the item whose first piece CTA c
 // held: slot 2c + 1, then slot 2c' of the CTAs c' up to the one that held its last
 // unit, in order. A warp takes a row: its lanes first read the pieces' maxima and
-// denominators, 32 at a time, then the sums, 16 bytes each (D = 64: two pieces at
-// once), several pieces in flight.
+// denominators, then the sums, 16 bytes each (D = 64: two pieces at once), eight
+// loads in flight.
 template <int D, int RB>
 __global__ void __launch_bounds__(32 * RB) kv4_join_kernel(const RowsArgs a) {
     constexpr int VL = D / 4;        // lanes of a row
@@ -646,23 +644,26 @@ __global__ void __launch_bounds__(32 * RB) kv4_join_kernel(const RowsArgs a) {
     float den = 0.0f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     const int sub = lane / VL, d4 = 4 * (lane % VL);
-    for (int p0 = 0; p0 < pieces; p0 += 32) {
+    constexpr int BATCH = 8 * PP;  // pieces in flight
+    for (int p0 = 0; p0 < pieces; p0 += BATCH) {
+        float4 x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {  // past the end: the last piece, not added
+            const float* sp = slot(min(p0 + q * PP + sub, pieces - 1)) + d4;  // 8-byte aligned
+            const float2 lo = *reinterpret_cast<const float2*>(sp), hi = *reinterpret_cast<const float2*>(sp + 2);
+            x[q] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
         float f = 0.0f, d = 0.0f;
-        if (p0 + lane < pieces) {
+        if (lane < BATCH && p0 + lane < pieces) {
             const float2 st = *reinterpret_cast<const float2*>(slot(p0 + lane) + D);
             f = st.x == -INFINITY ? (st.y != st.y ? 1.0f : 0.0f) : exp2_approx(st.x - m);
             d = f * st.y;
         }
         den += warp_sum(d);
-        const int n = min(32, pieces - p0);
-#pragma unroll 8
-        for (int q = 0; q < n; q += PP) {
-            const float g = __shfl_sync(0xffffffffu, f, q + sub);
-            if (q + sub < n) {
-                const float* sp = slot(p0 + q + sub) + d4;  // 8-byte aligned
-                const float2 x = *reinterpret_cast<const float2*>(sp), y = *reinterpret_cast<const float2*>(sp + 2);
-                v.x += g * x.x, v.y += g * x.y, v.z += g * y.x, v.w += g * y.y;
-            }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float g = __shfl_sync(0xffffffffu, f, q * PP + sub);
+            if (p0 + q * PP + sub < pieces) v.x += g * x[q].x, v.y += g * x[q].y, v.z += g * x[q].z, v.w += g * x[q].w;
         }
     }
     if (PP == 2) {
