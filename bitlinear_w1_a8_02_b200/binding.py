@@ -7,6 +7,7 @@ library is missing or fails to load, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from contextlib import nullcontext
 from typing import Optional
@@ -95,6 +96,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(index: int) -> int:
+    """Handle of the current stream of CUDA device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _check(st: int, where: str):
@@ -294,34 +300,42 @@ def forward_int8(Wq: torch.Tensor, wstep: torch.Tensor, x: torch.Tensor, rmsnorm
                  ws: Optional[torch.Tensor] = None):
     """One 8-bit linear layer of x [M, K] bf16 (after a unit-weight RMSNorm if asked): y [M, N] in out_dtype (bf16 or
     fp32), and the int32 accumulator with want_acc. Scratch is allocated per call unless `ws` is given."""
-    _cuda(Wq, "Wq", torch.int8)
-    _cuda(wstep, "wstep", torch.float32)
-    _cuda(x, "x", torch.bfloat16)
     N, K = Wq.shape
     M = x.shape[0]
-    if x.shape != (M, K) or wstep.shape != (N,):
-        raise ValueError("shapes of Wq, wstep and x do not match")
-    dev = x.device
-    if Wq.device != dev or wstep.device != dev:
-        raise ValueError("Wq, wstep and x must be on one device")
+    index = x.get_device()
+    for t, name, dt, shape in ((Wq, "Wq", torch.int8, (N, K)), (wstep, "wstep", torch.float32, (N,)),
+                               (x, "x", torch.bfloat16, (M, K)), (residual, "residual", torch.bfloat16, (M, N)),
+                               (out, "out", None, (M, N))):
+        if t is not None and (t.dtype is not dt and dt is not None or t.shape != shape or t.get_device() != index or
+                              index < 0 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dt or 'bf16 or fp32'} CUDA tensor {shape} on the device of x, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("out_dtype must be bf16 or fp32")
-    for t, name, dt in ((residual, "residual", torch.bfloat16), (out, "out", out_dtype)):
-        if t is not None and (_cuda(t, name, dt).shape != (M, N) or t.device != dev):
-            raise ValueError(f"{name} must be [{M}, {N}] on {dev}")
-    here = dev.index == torch.cuda.current_device()
-    with nullcontext() if here else torch.cuda.device(dev):
-        y = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
-        acc = torch.empty((M, N), dtype=torch.int32, device=dev) if want_acc else None
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("the output must be bf16 or fp32")
+    with _HERE if index == torch.cuda.current_device() else torch.cuda.device(index):
+        if out is None:
+            out = (x if out_dtype is torch.bfloat16 else wstep).new_empty((M, N))
+        acc = torch.empty((M, N), dtype=torch.int32, device=x.device) if want_acc else None
         if ws is None:
-            ws = torch.empty(workspace_bytes(BL_OP_FORWARD, M, N, K), dtype=torch.uint8, device=dev)
-        st = lib().bitlinear_forward_int8(_ptr(Wq), _ptr(wstep), N, K, _ptr(x), M, int(bool(rmsnorm)), _ptr(residual),
-                                          _ptr(y), BL_FP32 if out_dtype == torch.float32 else BL_BF16, _ptr(acc),
-                                          _ptr(ws), ws.numel(), _stream(dev))
-    _check(st, "bitlinear_forward_int8")
-    return (y, acc) if want_acc else y
+            ws = Wq.new_empty(_forward_bytes(M, N, K))
+        st = lib().bitlinear_forward_int8(Wq.data_ptr(), wstep.data_ptr(), N, K, x.data_ptr(), M, 1 if rmsnorm else 0,
+                                          None if residual is None else residual.data_ptr(), out.data_ptr(),
+                                          BL_FP32 if out_dtype is torch.float32 else BL_BF16,
+                                          None if acc is None else acc.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                          _raw_stream(index))
+    if st:
+        _check(st, "bitlinear_forward_int8")
+    return (out, acc) if want_acc else out
+
+
+_HERE = nullcontext()
+
+
+@functools.lru_cache(maxsize=4096)
+def _forward_bytes(M: int, N: int, K: int) -> int:
+    return workspace_bytes(BL_OP_FORWARD, M, N, K)
 
 
 def validate_packed(Wp: torch.Tensor) -> int:

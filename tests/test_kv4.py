@@ -1,7 +1,5 @@
 """The 4-bit paged cache and the attention over it: codes, steps and rotated queries bit for bit
 against the definition, attention against 64 bits, refusals on the host."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -56,8 +54,8 @@ def _call(fn, **kw):
              cache=True, batch=True)
     for k, v in kw.items():
         next(d for d in (c, b, a) if k in d)[k] = v
-    C = ctypes.byref(kv4._CacheStruct(*c.values())) if a["cache"] else None
-    B = ctypes.byref(kv4._BatchStruct(*b.values())) if a["batch"] else None
+    C = kv4._pack_cache(*[x or 0 for x in c.values()], 0) if a["cache"] else None
+    B = kv4._pack_batch(*[x or 0 for x in b.values()]) if a["batch"] else None
     L = bl.lib()
     if fn == "append":
         return L.bitlinear_kv4_append(a["q"], a["q_stride"], a["k"], a["k_stride"], a["v"], a["v_stride"], a["M"], a["Hq"],
