@@ -15,6 +15,7 @@ namespace bl {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kFewTokens = 512;  // below: one step a warp
 
 struct AppendArgs {
     const uint16_t *q, *k, *v;
@@ -24,7 +25,7 @@ struct AppendArgs {
     int64_t max_pos;
     Kv4View cache;
     Kv4Seqs batch;
-    int M, Hq, warps_per_token;
+    int M, Hq;
     int interleaved;
     unsigned* err;
 };
@@ -38,58 +39,65 @@ __device__ __forceinline__ void unpack_octet(const uint4& v, float (&f)[8]) {
     }
 }
 
-// Rotate the octet `o` (dims 8 o ..) of a vector held by D/8 adjacent lanes. Every
-// lane of the warp calls it.
-template <int D>
-__device__ __forceinline__ void rotate_octet(const uint4& raw, int o, const float* row, bool interleaved, float (&r)[8]) {
-    constexpr int LPV = D / 8;
-    float x[8];
-    unpack_octet(raw, x);
-    if (interleaved) {
-        const float4 c = *reinterpret_cast<const float4*>(row + 4 * o);
-        const float4 s = *reinterpret_cast<const float4*>(row + D / 2 + 4 * o);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = x[2 * j], b = x[2 * j + 1];
-            r[2 * j] = __fsub_rn(__fmul_rn(a, cc[j]), __fmul_rn(b, ss[j]));
-            r[2 * j + 1] = __fadd_rn(__fmul_rn(b, cc[j]), __fmul_rn(a, ss[j]));
-        }
-        return;
-    }
-    uint4 other;
-    other.x = __shfl_xor_sync(0xffffffffu, raw.x, LPV / 2);
-    other.y = __shfl_xor_sync(0xffffffffu, raw.y, LPV / 2);
-    other.z = __shfl_xor_sync(0xffffffffu, raw.z, LPV / 2);
-    other.w = __shfl_xor_sync(0xffffffffu, raw.w, LPV / 2);
-    float p[8];
-    unpack_octet(other, p);
-    const bool low = o < LPV / 2;  // this lane holds the a of its pairs
-    const int i = 8 * (o & (LPV / 2 - 1));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * h);
-        const float4 s = *reinterpret_cast<const float4*>(row + D / 2 + i + 4 * h);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float own = __fmul_rn(x[4 * h + j], cc[j]), oth = __fmul_rn(p[4 * h + j], ss[j]);
-            r[4 * h + j] = low ? __fsub_rn(own, oth) : __fadd_rn(own, oth);
-        }
-    }
-}
+// The rotation of a lane's octet `o` (dims 8 o ..): r = fl(fl(x c) + fl(partner s)), with the sign of the
+// partner's product in s (a product's rounding does not depend on its sign).
+struct Turn {
+    float c[8], s[8];
+};
 
 template <int D>
+__device__ __forceinline__ Turn load_turn(const float* row, int o, bool interleaved) {
+    Turn t;
+    if (interleaved) {  // pair j of the octet: entry 4 o + j, for both of its dims
+        const float4 c = *reinterpret_cast<const float4*>(row + 4 * o), s = *reinterpret_cast<const float4*>(row + D / 2 + 4 * o);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.c[2 * j] = t.c[2 * j + 1] = cc[j], t.s[2 * j] = -ss[j], t.s[2 * j + 1] = ss[j];
+        return t;
+    }
+    const int i = 8 * (o & (D / 16 - 1));
+    const bool low = o < D / 16;  // the octet holds the a of its pairs
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * h), s = *reinterpret_cast<const float4*>(row + D / 2 + i + 4 * h);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.c[4 * h + j] = cc[j], t.s[4 * h + j] = low ? -ss[j] : ss[j];
+    }
+    return t;
+}
+
+// Rotate an octet of a vector held by D/8 adjacent lanes. Every lane of the warp calls it.
+template <int D>
+__device__ __forceinline__ void rotate_octet(const uint4& raw, const Turn& t, bool interleaved, float (&r)[8]) {
+    float x[8], p[8];
+    unpack_octet(raw, x);
+    if (interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = x[j ^ 1];
+    } else {
+        uint4 other;
+        other.x = __shfl_xor_sync(0xffffffffu, raw.x, D / 16);
+        other.y = __shfl_xor_sync(0xffffffffu, raw.y, D / 16);
+        other.z = __shfl_xor_sync(0xffffffffu, raw.z, D / 16);
+        other.w = __shfl_xor_sync(0xffffffffu, raw.w, D / 16);
+        unpack_octet(other, p);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = __fadd_rn(__fmul_rn(x[j], t.c[j]), __fmul_rn(p[j], t.s[j]));
+}
+
+// Block (x, m): warps of token m. A warp takes STEPS times 32 octets: with several steps the search for the
+// token's sequence and the rotation row (a lane's octet of a vector is the same in every step) are shared, with
+// one step there are the most warps, for few tokens.
+template <int D, int STEPS>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
     constexpr int LPV = D / 8;  // lanes of a vector
     constexpr int G = D / kKvGroup;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t gw = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int m = (int)(gw / a.warps_per_token);
-    if (m >= a.M) return;
-    const int item = (int)(gw % a.warps_per_token) * 32 + lane;  // lane of the token
+    const int lane = threadIdx.x & 31, m = blockIdx.y;
+    const int first = (int)(blockIdx.x * blockDim.x + threadIdx.x - lane) * STEPS + lane;  // octet of the token
 
     const int s = kv4_seq_of_row(a.batch, m);
     if (s >= a.batch.S) return;  // padding
@@ -101,59 +109,68 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
         return;
     }
     if (pos < 0) return;  // no place in the cache: padding of an idle sequence
-    const float* row = a.cos_sin + pos * D;
-    const int kv_lanes = 2 * LPV * a.cache.hkv;
-    const bool is_kv = item < kv_lanes;
-    const bool is_q = !is_kv && item < kv_lanes + LPV * a.Hq;
-    const int o = item % LPV;  // octet of the vector
-    const int vec = is_kv ? item / LPV : (item - kv_lanes) / LPV;
-    const bool is_v = is_kv && (vec & 1);
-    const int head = is_kv ? vec >> 1 : vec;
-
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (is_kv)
-        raw = *reinterpret_cast<const uint4*>((is_v ? a.v + m * a.v_stride : a.k + m * a.k_stride) + head * D + 8 * o);
-    else if (is_q)
-        raw = *reinterpret_cast<const uint4*>(a.q + m * a.q_stride + head * D + 8 * o);
-    float x[8];
-    rotate_octet<D>(raw, o, row, a.interleaved != 0, x);
-    if (is_q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = f32_to_bf16_bits(x[2 * j]) | (uint32_t)f32_to_bf16_bits(x[2 * j + 1]) << 16;
-        *reinterpret_cast<uint4*>(a.q_out + m * a.qo_stride + head * D + 8 * o) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    // a warp without key or value lanes is done; the others stay together for the shuffles
-    if (!__any_sync(0xffffffffu, is_kv)) return;
-    if (is_v) unpack_octet(raw, x);
-    bool bad = false;
-    float top = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        bad |= !(fabsf(x[j]) < kKvHuge);
-        top = fmaxf(top, fabsf(x[j]));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const unsigned votes = __ballot_sync(0xffffffffu, bad && is_kv);
-    if (!is_kv) return;
-    // the key and value lanes of this token and head
-    const unsigned mine = LPV == 16 ? 0xffffffffu : 0xffffu << (lane & 16);
-    const bool marked = (votes & mine) != 0;
-    const float step = marked ? 0.0f : kv4_step(top);
-    const uint32_t word = kv4_word(x, step, !marked);
-    const int64_t at = kv4_vector(a.cache, a.batch, s, (int)pos, head);
-    if (at < 0) {
-        atomicOr(a.err, kErrBadBatch);
-        return;
-    }
+    const int kv_lanes = 2 * LPV * a.cache.hkv, all_lanes = kv_lanes + LPV * a.Hq;
+    const int o = lane % LPV;  // octet of the vector
     const int g = o >> 2, t = o & 3;
-    uint8_t* codes = is_v ? a.cache.vc : a.cache.kc;
-    uint16_t* steps = is_v ? a.cache.vs : a.cache.ks;
-    *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * (t * G + g)) = word;
-    if (t == 0)
-        steps[at * G + g] = marked && !is_v ? (uint16_t)0x7FC0 : (uint16_t)(__float_as_uint(step) >> 16);
+    const bool is_v = (lane / LPV) & 1;  // of the key and value octets: 32 is a multiple of 2 LPV
+    const bool interleaved = a.interleaved != 0;
+    const Turn turn = load_turn<D>(a.cos_sin + pos * D, o, interleaved);
+    const uint16_t* kv = (is_v ? a.v + m * a.v_stride : a.k + m * a.k_stride) + 8 * o;
+    const uint16_t* q = a.q + m * a.q_stride + 8 * o;
+    uint4 raw[STEPS];
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+        const int item = first + 32 * st;
+        raw[st] = make_uint4(0, 0, 0, 0);
+        if (item < kv_lanes)
+            raw[st] = *reinterpret_cast<const uint4*>(kv + item / (2 * LPV) * D);
+        else if (item < all_lanes)
+            raw[st] = *reinterpret_cast<const uint4*>(q + (item - kv_lanes) / LPV * D);
+    }
+    int64_t at = 0;  // this token's vector of head 0
+    if (first < kv_lanes) {
+        at = kv4_vector(a.cache, a.batch, s, (int)pos, 0);
+        if (at < 0) atomicOr(a.err, kErrBadBatch);
+    }
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+        const int item = first + 32 * st;
+        const bool is_kv = item < kv_lanes;
+        float x[8];
+        rotate_octet<D>(raw[st], turn, interleaved, x);
+        if (!is_kv && item < all_lanes)
+            *reinterpret_cast<uint4*>(a.q_out + m * a.qo_stride + (item - kv_lanes) / LPV * D + 8 * o) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        if (!__any_sync(0xffffffffu, is_kv)) continue;
+        if (is_v) unpack_octet(raw[st], x);
+        float top = fabsf(x[0]);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const unsigned votes = __ballot_sync(0xffffffffu, !(top < kKvHuge) && is_kv);
+        if (is_kv && at >= 0) {
+            // the key and value lanes of this token and head
+            const bool marked = (votes & (LPV == 16 ? 0xffffffffu : 0xffffu << (lane & 16))) != 0;
+            const float step = marked ? 0.0f : kv4_step(top);
+            const uint32_t word = step > 0.0f ? kv4_word(x, step) : 0x88888888u;
+            const int64_t vec = at + ((int64_t)(item / (2 * LPV)) << a.cache.page_shift);
+            *reinterpret_cast<uint32_t*>((is_v ? a.cache.vc : a.cache.kc) + vec * (D / 2) + 4 * (t * G + g)) = word;
+            if (t == 0)
+                (is_v ? a.cache.vs : a.cache.ks)[vec * G + g] =
+                    marked && !is_v ? (uint16_t)0x7FC0 : (uint16_t)(__float_as_uint(step) >> 16);
+        }
+        __syncwarp();
+    }
+}
+
+template <int D, int STEPS>
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+    const int octets = (2 * a.cache.hkv + a.Hq) * (D / 8);
+    const int warps = (octets + 32 * STEPS - 1) / (32 * STEPS);
+    const int per = warps < kThreads / 32 ? warps : kThreads / 32;
+    return launch_pdl(kv4_append_kernel<D, STEPS>, dim3((unsigned)((warps + per - 1) / per), (unsigned)a.M), dim3(32 * per), 0,
+                      s, a);
 }
 
 template <int D>
@@ -212,12 +229,11 @@ cudaError_t launch_kv4_append(const uint16_t* q, int64_t q_stride, const uint16_
     a.q_out = q_out, a.cos_sin = cos_sin, a.max_pos = max_pos;
     a.cache = cache, a.batch = batch;
     a.M = (int)M, a.Hq = Hq, a.interleaved = interleaved;
-    a.warps_per_token = ((2 * cache.hkv + Hq) * (D / 8) + 31) / 32;
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (M * a.warps_per_token + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_pdl(D == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                      s, a);
+    const bool few = M < kFewTokens;
+    if (D == 128) return few ? launch_append<128, 1>(a, s) : launch_append<128, 5>(a, s);
+    return few ? launch_append<64, 1>(a, s) : launch_append<64, 5>(a, s);
 }
 
 cudaError_t launch_kv4_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t M, int D, uint16_t* k, uint16_t* v,

@@ -31,16 +31,31 @@ __device__ __forceinline__ float kv4_step(float amax) {
     return __uint_as_float(b & ~0x7FFFFu);
 }
 
-// Eight values -> the word of their codes (n = c + 8); `live` 0 stores c = 0.
-__device__ __forceinline__ uint32_t kv4_word(const float (&x)[8], float step, bool live) {
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN stays
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Eight values of a group -> the word of their codes, n = 8 + rint(fl(x / step)) in bits 4j; step > 0, all finite.
+//
+// The quotient needs no division: q0 = fl(x r), r = fl(1 / step), and one Newton step q = fl(q0 + fl(x - q0 step) r)
+// give rint's argument to within 2^-46 before the last rounding, and that is enough for the same code. A tie is
+// x = T = (c + 1/2) step exactly, and then q = c + 1/2 exactly. Any other x is at least one unit of its last place
+// from T, which is mant(c + 1/2) / mant(T) units of c + 1/2's, and T has at most 9 bits: more than 0.5009 of a unit, so
+// neither the quotient nor q rounds onto the tie.
+// Adding 1.5 * 2^23 + 8 leaves n in the low bits; the words' upper parts add up to a constant.
+__device__ __forceinline__ uint32_t kv4_word(const float (&x)[8], float step) {
+    const float r = __frcp_rn(step);
     uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float c = live && step > 0.0f ? rintf(__fdiv_rn(x[j], step)) : 0.0f;
-        const int n = 8 + min(max((int)c, -7), 7);
-        w |= (uint32_t)n << (4 * j);
+    for (int j = 7; j >= 0; --j) {
+        const float q0 = __fmul_rn(x[j], r);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, step, x[j]), r, q0);
+        w = w * 16u + __float_as_uint(__fadd_rn(q, 12582920.0f));
     }
-    return w;
+    constexpr uint32_t upper = 0x4B400000u * 0x11111111u;  // sum of 0x4B400000 * 16^j, mod 2^32
+    return w - upper;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
@@ -53,6 +68,27 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+}
+
+// (lo, hi) -> bf16 pair
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bulk copy of global to shared memory, completion counted on `bar`; addresses and size multiples of 16.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
 }
 
 // (a & b) | c as one instruction. With two immediates the compiler makes two of it; the constants are passed as

@@ -71,13 +71,6 @@ struct RowsSmem {
     static size_t bytes(int S) { return FIXED + (size_t)(S + 1) * 4; }
 };
 
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
 // tc::mbar_wait with a hint that lets the warp sleep up to 20 us at a time: the polls of waiting warps take issue
 // slots from the unpacking ones.
 __device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) {
@@ -112,19 +105,6 @@ __device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// (lo, hi) -> bf16 pair
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
 

@@ -247,6 +247,36 @@ def test_append_bits(lens, D, H, Hk, P, interleaved):
 
 
 @gpu
+def test_append_ties_and_neighbours():
+    """Values on, just above and just below every half code, for every significand of the step, at several exponents."""
+    D, Hk, n = 128, 16, 64
+    b = Batch([(n, n)], D, Hk, Hk, 64)
+    k = np.zeros((n, Hk, D), np.float32)
+    for t in range(n):
+        for h in range(Hk):
+            step = np.float32((16 + h) * 2.0 ** (t % 32 - 20))
+            k[t, h, 0::32] = 7 * step  # the largest of each group: the step comes out as `step`
+            half = (np.arange(-6.5, 7.0, 1.0) * step).astype(np.float32)
+            for g, x in enumerate((half, np.nextafter(half, np.float32(np.inf)), np.nextafter(half, np.float32(-np.inf)), half)):
+                k[t, h, 32 * g + 1:32 * g + 15] = x
+    q, _, _ = b.qkv()
+    # bf16 inputs: half codes fit; their fp32 neighbours come from a rotation by an angle whose cosine is 1 +- 2^-23
+    cs = torch.zeros((n, D), device="cuda")
+    cs[:, :D // 2] = 1.0
+    for c in (1.0, float(np.nextafter(np.float32(1), np.float32(2))), float(np.nextafter(np.float32(1), np.float32(0)))):
+        cs[:, 1:15] = c
+        cs[:, 33:47] = c
+        kk = torch.from_numpy(k).to(torch.bfloat16).cuda()
+        bl.kv4_append(q, kk, kk, cs, *b.args())
+        kc, ks, vc, vs = ref.entry(ref.rotate(np_(kk.float()), np_(cs)[:, None]), np_(kk.float()))
+        page = b.table[0, np.arange(n) // 64]
+        for have, want in ((b.cache.k_codes, ref.pack(kc)), (b.cache.v_codes, ref.pack(vc))):
+            assert np.array_equal(np_(have)[page, :, np.arange(n) % 64], want)
+        for have, want in ((b.cache.k_steps, ks), (b.cache.v_steps, vs)):
+            assert np.array_equal(np_(have.float())[page, :, np.arange(n) % 64], want)
+
+
+@gpu
 def test_append_in_place_and_idle_sequences():
     lens = [(1, 4), (1, 0), (3, 2)]  # an idle sequence; one whose first token has no position
     b = Batch(lens, 128, 8, 2, 16)
