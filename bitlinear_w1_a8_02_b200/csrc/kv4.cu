@@ -87,7 +87,7 @@ __device__ __forceinline__ void rotate_octet(const uint4& raw, const Turn& t, bo
     for (int j = 0; j < 8; ++j) r[j] = __fadd_rn(__fmul_rn(x[j], t.c[j]), __fmul_rn(p[j], t.s[j]));
 }
 
-// Block (x, m): warps of token m. A warp takes STEPS times 32 octets: with several steps the search for the
+// Threads (x, m): warps of token m. A warp takes STEPS times 32 octets: with several steps the search for the
 // token's sequence and the rotation row (a lane's octet of a vector is the same in every step) are shared, with
 // one step there are the most warps, for few tokens.
 template <int D, int STEPS>
@@ -96,9 +96,27 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     constexpr int G = D / kKvGroup;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int lane = threadIdx.x & 31, m = blockIdx.y;
-    const int first = (int)(blockIdx.x * blockDim.x + threadIdx.x - lane) * STEPS + lane;  // octet of the token
+    const int lane = threadIdx.x & 31, m = blockIdx.y * blockDim.y + threadIdx.y;
+    // octets first + stride st of the token: every warp has its share of the keys and values, which cost more
+    const int first = (int)(blockIdx.x * blockDim.x + threadIdx.x), stride = (int)(gridDim.x * blockDim.x);
 
+    if (m >= a.M) return;
+    const int kv_lanes = 2 * LPV * a.cache.hkv, all_lanes = kv_lanes + LPV * a.Hq;
+    const int o = lane % LPV;  // octet of the vector
+    const int g = o >> 2, t = o & 3;
+    const bool is_v = (lane / LPV) & 1;  // of the key and value octets: 32 is a multiple of 2 LPV
+    const uint16_t* kv = (is_v ? a.v + m * a.v_stride : a.k + m * a.k_stride) + 8 * o;
+    const uint16_t* q = a.q + m * a.q_stride + 8 * o;
+    uint4 raw[STEPS];  // under way while the token's place is looked up
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+        const int item = first + stride * st;
+        raw[st] = make_uint4(0, 0, 0, 0);
+        if (item < kv_lanes)
+            raw[st] = *reinterpret_cast<const uint4*>(kv + item / (2 * LPV) * D);
+        else if (item < all_lanes)
+            raw[st] = *reinterpret_cast<const uint4*>(q + (item - kv_lanes) / LPV * D);
+    }
     const int s = kv4_seq_of_row(a.batch, m);
     if (s >= a.batch.S) return;  // padding
     const int n_end = a.batch.q_start[s + 1], len = a.batch.kv_len[s];
@@ -109,24 +127,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
         return;
     }
     if (pos < 0) return;  // no place in the cache: padding of an idle sequence
-    const int kv_lanes = 2 * LPV * a.cache.hkv, all_lanes = kv_lanes + LPV * a.Hq;
-    const int o = lane % LPV;  // octet of the vector
-    const int g = o >> 2, t = o & 3;
-    const bool is_v = (lane / LPV) & 1;  // of the key and value octets: 32 is a multiple of 2 LPV
     const bool interleaved = a.interleaved != 0;
     const Turn turn = load_turn<D>(a.cos_sin + pos * D, o, interleaved);
-    const uint16_t* kv = (is_v ? a.v + m * a.v_stride : a.k + m * a.k_stride) + 8 * o;
-    const uint16_t* q = a.q + m * a.q_stride + 8 * o;
-    uint4 raw[STEPS];
-#pragma unroll
-    for (int st = 0; st < STEPS; ++st) {
-        const int item = first + 32 * st;
-        raw[st] = make_uint4(0, 0, 0, 0);
-        if (item < kv_lanes)
-            raw[st] = *reinterpret_cast<const uint4*>(kv + item / (2 * LPV) * D);
-        else if (item < all_lanes)
-            raw[st] = *reinterpret_cast<const uint4*>(q + (item - kv_lanes) / LPV * D);
-    }
     int64_t at = 0;  // this token's vector of head 0
     if (first < kv_lanes) {
         at = kv4_vector(a.cache, a.batch, s, (int)pos, 0);
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     }
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
-        const int item = first + 32 * st;
+        const int item = first + stride * st;
         const bool is_kv = item < kv_lanes;
         float x[8];
         rotate_octet<D>(raw[st], turn, interleaved, x);
@@ -164,57 +166,86 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     }
 }
 
+// Blocks of at most 8 warps: x the warps of a token, y tokens (a single warp a token is too small a block).
+struct Shape {
+    dim3 grid, block;
+};
+Shape shape_of(int warps, int64_t M, bool one_token) {
+    const int x = warps < kThreads / 32 ? warps : kThreads / 32, y = one_token ? 1 : kThreads / 32 / x;
+    return {dim3((unsigned)((warps + x - 1) / x), (unsigned)((M + y - 1) / y)), dim3(32 * x, y)};
+}
+
 template <int D, int STEPS>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     const int octets = (2 * a.cache.hkv + a.Hq) * (D / 8);
     const int warps = (octets + 32 * STEPS - 1) / (32 * STEPS);
-    const int per = warps < kThreads / 32 ? warps : kThreads / 32;
-    return launch_pdl(kv4_append_kernel<D, STEPS>, dim3((unsigned)((warps + per - 1) / per), (unsigned)a.M), dim3(32 * per), 0,
-                      s, a);
+    const Shape g = shape_of(warps, a.M, true);
+    return launch_pdl(kv4_append_kernel<D, STEPS>, g.grid, g.block, 0, s, a);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4View cache, const Kv4Seqs batch, int M,
-                                                            int warps_per_token, uint16_t* k, uint16_t* v, unsigned* err) {
+// Threads (x, m): octets of token m, one a lane; a warp takes STEPS times 32.
+template <int D, int STEPS>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4View cache, const Kv4Seqs batch, int M, uint16_t* k,
+                                                            uint16_t* v, unsigned* err) {
     constexpr int LPV = D / 8;
     constexpr int G = D / kKvGroup;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t gw = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int m = (int)(gw / warps_per_token);
+    const int lane = threadIdx.x & 31, m = blockIdx.y * blockDim.y + threadIdx.y;
+    const int first = (int)(blockIdx.x * blockDim.x + threadIdx.x - lane) * STEPS + lane;
     if (m >= M) return;
-    const int item = (int)(gw % warps_per_token) * 32 + lane;
     const int s = kv4_seq_of_row(batch, m);
     if (s >= batch.S) return;
-    const int n_end = batch.q_start[s + 1];
-    const int64_t pos = (int64_t)batch.kv_len[s] - n_end + m;
-    if (batch.kv_len[s] < 0 || m < batch.q_start[s] || n_end > M || pos >= ((int64_t)batch.W << cache.page_shift)) {
+    const int n_end = batch.q_start[s + 1], len = batch.kv_len[s];
+    const int64_t pos = (int64_t)len - n_end + m;
+    if (len < 0 || m < batch.q_start[s] || n_end > M || pos >= ((int64_t)batch.W << cache.page_shift)) {
         if (lane == 0) atomicOr(err, kErrBadBatch);
         return;
     }
     if (pos < 0) return;
-    if (item >= 2 * LPV * cache.hkv) return;
-    const int o = item % LPV, vec = item / LPV, head = vec >> 1;
-    const bool is_v = vec & 1;
-    const int64_t at = kv4_vector(cache, batch, s, (int)pos, head);
+    const int64_t at = kv4_vector(cache, batch, s, (int)pos, 0);
     if (at < 0) {
-        atomicOr(err, kErrBadBatch);
+        if (lane == 0) atomicOr(err, kErrBadBatch);
         return;
     }
-    const int g = o >> 2, t = o & 3;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>((is_v ? cache.vc : cache.kc) + at * (D / 2) + 4 * (t * G + g));
-    uint32_t st = (is_v ? cache.vs : cache.ks)[at * G + g];
-    st |= st << 16;
-    const uint32_t s16 = bf16x2_mul(st, kBf16x2Sixteen), s24 = bf16x2_mul(st, kBf16x2MinusTwentyFour);
-    uint32_t p[4];  // pairs (i, i + 4)
-    p[0] = bf16x2_fma(kv4_unit_pair<0>(w), s16, s24);
-    p[1] = bf16x2_fma(kv4_unit_pair<1>(w), s16, s24);
-    p[2] = bf16x2_fma(kv4_unit_pair<2>(w), s16, s24);
-    p[3] = bf16x2_fma(kv4_unit_pair<3>(w), s16, s24);
-    const uint4 out = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
-                                 __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
-    *reinterpret_cast<uint4*>((is_v ? v : k) + ((int64_t)m * cache.hkv + head) * D + 8 * o) = out;
+    const int o = lane % LPV, g = o >> 2, t = o & 3;
+    const bool is_v = (lane / LPV) & 1;
+    const uint8_t* codes = (is_v ? cache.vc : cache.kc) + at * (D / 2) + 4 * (t * G + g);
+    const uint16_t* steps = (is_v ? cache.vs : cache.ks) + at * G + g;
+    uint16_t* out = (is_v ? v : k) + (int64_t)m * cache.hkv * D + 8 * o;
+    const int64_t head_vecs = (int64_t)1 << cache.page_shift;
+    uint32_t w[STEPS], st[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int head = (first + 32 * i) / (2 * LPV);
+        if (head < cache.hkv) {
+            w[i] = *reinterpret_cast<const uint32_t*>(codes + head * head_vecs * (D / 2));
+            st[i] = steps[head * head_vecs * G];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int head = (first + 32 * i) / (2 * LPV);
+        if (head >= cache.hkv) return;
+        const uint32_t ss = st[i] | st[i] << 16;
+        const uint32_t s16 = bf16x2_mul(ss, kBf16x2Sixteen), s24 = bf16x2_mul(ss, kBf16x2MinusTwentyFour);
+        uint32_t p[4];  // pairs (i, i + 4)
+        p[0] = bf16x2_fma(kv4_unit_pair<0>(w[i]), s16, s24);
+        p[1] = bf16x2_fma(kv4_unit_pair<1>(w[i]), s16, s24);
+        p[2] = bf16x2_fma(kv4_unit_pair<2>(w[i]), s16, s24);
+        p[3] = bf16x2_fma(kv4_unit_pair<3>(w[i]), s16, s24);
+        *reinterpret_cast<uint4*>(out + head * D) =
+            make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410), __byte_perm(p[0], p[1], 0x7632),
+                       __byte_perm(p[2], p[3], 0x7632));
+    }
+}
+
+template <int D, int STEPS>
+cudaError_t launch_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t M, uint16_t* k, uint16_t* v, unsigned* err,
+                        cudaStream_t s) {
+    const int warps = (2 * cache.hkv * (D / 8) + 32 * STEPS - 1) / (32 * STEPS);
+    const Shape g = shape_of(warps, M, false);
+    return launch_pdl(kv4_read_kernel<D, STEPS>, g.grid, g.block, 0, s, cache, batch, (int)M, k, v, err);
 }
 
 }  // namespace
@@ -241,10 +272,9 @@ cudaError_t launch_kv4_read(const Kv4View& cache, const Kv4Seqs& batch, int64_t 
     unsigned* err = nullptr;
     cudaError_t e = device_error_word(&err);
     if (e != cudaSuccess) return e;
-    const int wpt = (2 * cache.hkv * (D / 8) + 31) / 32;
-    const int64_t blocks = (M * wpt + kThreads / 32 - 1) / (kThreads / 32);
-    return launch_pdl(D == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
-                      cache, batch, (int)M, wpt, k, v, err);
+    const bool few = M < kFewTokens;
+    if (D == 128) return few ? launch_read<128, 1>(cache, batch, M, k, v, err, s) : launch_read<128, 5>(cache, batch, M, k, v, err, s);
+    return few ? launch_read<64, 1>(cache, batch, M, k, v, err, s) : launch_read<64, 5>(cache, batch, M, k, v, err, s);
 }
 
 }  // namespace bl

@@ -382,7 +382,7 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
  * Batch. S sequences, their new tokens stacked in M rows:
  *   q_start     [S + 1] device int32: rows q_start[s] .. q_start[s+1] - 1 belong to
  *               sequence s; not decreasing, q_start[0] = 0, q_start[S] <= M. Rows at or after
- *               q_start[S] are padding: nothing is read for them or written to them.
+ *               q_start[S] are padding: nothing is written to them.
  *   kv_len      [S] device int32: tokens of the sequence in the cache, the new
  *               ones included. New token i of n has position kv_len - n + i; one
  *               whose position is negative (an idle sequence, kv_len 0) is not
