@@ -712,7 +712,6 @@ BL_API bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, in
     cudaStream_t s = (cudaStream_t)stream;
     int8_t* xq = (int8_t*)((char*)ws + w.xq);
     float* scale = (float*)((char*)ws + w.scale);
-    BL_TRY(bl::launch_act_quant(x, M, K, bl::XQ_NATURAL, xq, scale, nullptr, s, rmsnorm != 0));
-    return cuda_status(bl::launch_int8(Wq, wstep, N, K, xq, scale, M, residual, ydt == BL_BF16 ? (uint16_t*)y : nullptr,
+    return cuda_status(bl::launch_int8(Wq, wstep, N, K, x, rmsnorm != 0, xq, scale, M, residual, ydt == BL_BF16 ? (uint16_t*)y : nullptr,
                                        ydt == BL_FP32 ? (float*)y : nullptr, acc, s));
 }

@@ -3,10 +3,11 @@
 //
 //   y[m, n] = [residual +] fl(fl(float(acc) wstep[n]) fl(1 / s_m))
 //
-// M <= 16 tokens: bound by the N K weight bytes. A warp owns 16 rows and streams
-// them from DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A):
-// a lane's 16 bytes of a row are the four words of two MMAs, and the lane's 16
-// bytes of a token's codes line up with them, so neither side is rearranged.
+// M <= 16 tokens: bound by the N K weight bytes. Warps stream 16 rows at a time
+// from DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A): a
+// lane's 16 bytes of a row are the four words of two MMAs, and the lane's 16 bytes
+// of a token's codes line up with them, so neither side is rearranged. Up to four
+// tokens are quantised inside the kernel, by every block for itself.
 #include <algorithm>
 
 #include "common.cuh"
@@ -87,82 +88,153 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 
 constexpr int kGemvWarps = 8;
+constexpr int kUnroll = 5;               // 64-byte chunks of a row pair in flight per warp
+constexpr int kFusedTokens = 4;          // up to here the kernel quantises x itself
+constexpr int kFusedBytes = 40 * 1024;   // and keeps its codes in shared memory
 
-// CTA: KS warps share a 16-row tile (64-byte chunks of K in turn), kGemvWarps / KS tiles.
-template <int NT, int KS>
-__global__ void __launch_bounds__(32 * kGemvWarps) gemv_int8_kernel(const Int8Args a) {
-    constexpr int TILES = kGemvWarps / KS;
-    constexpr int U = 4;
-    __shared__ int part[kGemvWarps][NT * 4][32];
-    grid_dependency_wait();
-    grid_dependents_launch();
+struct GemvIn {
+    const uint16_t* x;  // fused: activations to quantise
+    int norm;
+    int pitch;          // fused: bytes from one token's codes to the next
+};
+
+// The kernel's blocks are persistent and take every gridDim.x-th tile of 16 rows; the 8 warps of a block share a
+// tile (64-byte chunks of K in turn), their sums meet in shared memory. The first tile's weights are under way before
+// the kernel waits for the one before it: weights are constants (the header says so for packed weights).
+template <int NT, bool FUSED>
+__global__ void __launch_bounds__(32 * kGemvWarps, NT == 1 ? 4 : 3) gemv_int8_kernel(const Int8Args a, const GemvIn in) {
+    __shared__ int part[2][kGemvWarps][NT * 4][32];
+    __shared__ float xstep_sh[8 * NT];
+    __shared__ float fscratch[kGemvWarps];
+    __shared__ double dscratch[kGemvWarps];
+    extern __shared__ __align__(16) int8_t codes[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, t = lane & 3;
-    const int tile = blockIdx.x * TILES + warp / KS, ks = warp % KS;
-    const int n0 = tile * 16;
-    const int chunks = (a.K + 63) / 64;
-    int d[NT][4];
+    const int tiles = (a.N + 15) / 16;
+    const int n_chunks = (a.K + 63) / 64;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 u[kUnroll], v[kUnroll];
+    // chunks c, c + 8, ... of tile `tile`; rows past the end read row N - 1, and their sums are not stored
+    auto load = [&](int tile, int c) {
+        const int8_t* w0 = a.Wq + (int64_t)min(tile * 16 + r, a.N - 1) * a.K + 16 * t;
+        const int8_t* w1 = a.Wq + (int64_t)min(tile * 16 + r + 8, a.N - 1) * a.K + 16 * t;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
-    if (n0 < a.N) {
-        // rows past the end read row N - 1; their sums are not stored
-        const int8_t* w0 = a.Wq + (int64_t)min(n0 + r, a.N - 1) * a.K + 16 * t;
-        const int8_t* w1 = a.Wq + (int64_t)min(n0 + r + 8, a.N - 1) * a.K + 16 * t;
-        const int8_t* x[NT];
-        bool live[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            live[nt] = nt * 8 + r < a.M;
-            x[nt] = a.xq + (int64_t)min(nt * 8 + r, a.M - 1) * a.K + 16 * t;
+        for (int i = 0; i < kUnroll; ++i) {
+            const int k = (c + i * kGemvWarps) * 64;
+            const bool in_k = k + 16 * t < a.K;  // K is a multiple of 16
+            u[i] = in_k ? ld_stream16(w0 + k) : zero;
+            v[i] = in_k ? ld_stream16(w1 + k) : zero;
         }
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int c = ks; c < chunks; c += KS * U) {
-            uint4 u[U], v[U], b[U][NT];
+    };
+    load(blockIdx.x, warp);
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    if (FUSED) {
+        // as the separate quantiser does it
+        for (int m = 0; m < a.M; ++m) {
+            const uint4* xr = reinterpret_cast<const uint4*>(in.x + (int64_t)m * a.K);
+            float top = 0.0f;
+            double ss = 0.0;
+            for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
+                const uint4 w = xr[c];
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int k = (c + i * KS) * 64;
-                const bool in = k + 16 * t < a.K;  // K is a multiple of 16
-                u[i] = in ? ld_stream16(w0 + k) : zero;
-                v[i] = in ? ld_stream16(w1 + k) : zero;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[i][nt] = in && live[nt] ? *reinterpret_cast<const uint4*>(x[nt] + k) : zero;
+                for (int e = 0; e < 4; ++e) {
+                    const float lo = __uint_as_float(ws[e] << 16), hi = __uint_as_float(ws[e] & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+                    if (in.norm) ss = __fma_rn((double)lo, (double)lo, __fma_rn((double)hi, (double)hi, ss));
+                }
             }
+            top = block_max<kGemvWarps>(top, fscratch);
+            float rms = 1.0f;
+            if (in.norm) {
+                ss = block_sum<kGemvWarps>(ss, dscratch);
+                rms = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn((float)(ss / (double)a.K), kRmsEps)));
+                top = __fmul_rn(top, rms);
+            }
+            const float s = __fdiv_rn(kActRange, fmaxf(top, kActEps));
+            if (threadIdx.x == 0) xstep_sh[m] = __fdiv_rn(1.0f, s);
+            for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
+                const uint4 w = xr[c];
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+                for (int e = 0; e < 8; ++e) {
+                    float f = __uint_as_float(e & 1 ? ws[e / 2] & 0xffff0000u : ws[e / 2] << 16);
+                    if (in.norm) f = __fmul_rn(f, rms);
+                    o[e / 4] |= (uint32_t)(quant_code(f, s) & 255) << (8 * (e & 3));
+                }
+                *reinterpret_cast<uint2*>(codes + m * in.pitch + 8 * c) = make_uint2(o[0], o[1]);
+            }
+        }
+    } else if (threadIdx.x < a.M) {
+        xstep_sh[threadIdx.x] = __fdiv_rn(1.0f, a.scale[threadIdx.x]);
+    }
+    __syncthreads();
+
+    const int8_t* x[NT];
+    bool live[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        live[nt] = nt * 8 + r < a.M;
+        const int m = min(nt * 8 + r, a.M - 1);
+        x[nt] = (FUSED ? codes + m * in.pitch : a.xq + (int64_t)m * a.K) + 16 * t;
+    }
+    int turn = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+        // the output this thread stores after the sums have met: element e = warp of nt = 0 .. NT - 1
+        const int n = tile * 16 + r + 8 * ((warp & 3) >> 1);
+        const float ws = warp < 4 * NT && n < a.N ? a.wstep[n] : 0.0f;
+        int d[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
+        for (int c = warp; c < n_chunks; c += kGemvWarps * kUnroll) {
+            if (c != warp || tile != blockIdx.x) load(tile, c);
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                const int k = (c + i * kGemvWarps) * 64;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_s8(d[nt], u[i].x, v[i].x, u[i].y, v[i].y, b[i][nt].x, b[i][nt].y);
-                    mma_s8(d[nt], u[i].z, v[i].z, u[i].w, v[i].w, b[i][nt].z, b[i][nt].w);
+                    const uint4 b = k + 16 * t < a.K && live[nt] ? *reinterpret_cast<const uint4*>(x[nt] + k) : zero;
+                    mma_s8(d[nt], u[i].x, v[i].x, u[i].y, v[i].y, b.x, b.y);
+                    mma_s8(d[nt], u[i].z, v[i].z, u[i].w, v[i].w, b.z, b.w);
                 }
+            }
         }
-    }
-    if (KS > 1) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[warp][nt * 4 + e][lane] = d[nt][e];
-        __syncthreads();
-        if (ks != 0) return;
+            for (int e = 0; e < 4; ++e) part[turn][warp][nt * 4 + e][lane] = d[nt][e];
+        __syncthreads();  // the other half of `part` is free: every warp has passed the tile before
+        if (warp < 4 * NT) {
+            int acc = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                for (int w = 1; w < KS; ++w) d[nt][e] += part[warp + w][nt * 4 + e][lane];
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = n0 + r + 8 * (e >> 1), m = nt * 8 + 2 * t + (e & 1);
-            if (n < a.N && m < a.M) store_one(a, m, n, d[nt][e], a.wstep[n], __fdiv_rn(1.0f, a.scale[m]));
+            for (int w = 0; w < kGemvWarps; ++w) acc += part[turn][w][warp][lane];
+            const int m = (warp >> 2) * 8 + 2 * t + (warp & 1);
+            if (n < a.N && m < a.M) store_one(a, m, n, acc, ws, xstep_sh[m]);
         }
+    }
 }
 
-template <int NT>
-cudaError_t launch_gemv_nt(const Int8Args& a, cudaStream_t s) {
+template <int NT, bool FUSED>
+cudaError_t launch_gemv_nt(const Int8Args& a, const GemvIn& in, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static int resident[64];  // blocks the device holds at once
+    if (dev >= 64 || !resident[dev]) {
+        int sms = 0, per = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, gemv_int8_kernel<NT, FUSED>, 32 * kGemvWarps, FUSED ? 8192 : 0);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) resident[dev] = sms * per;
+    }
     const int tiles = (a.N + 15) / 16;
-    if (tiles >= 148 * 8) return launch_pdl(gemv_int8_kernel<NT, 1>, dim3((tiles + 7) / 8), dim3(256), 0, s, a);
-    return launch_pdl(gemv_int8_kernel<NT, 8>, dim3(tiles), dim3(256), 0, s, a);
+    const int grid = std::min(tiles, dev < 64 ? resident[dev] : 148);
+    return launch_pdl(gemv_int8_kernel<NT, FUSED>, dim3((unsigned)grid), dim3(32 * kGemvWarps),
+                      FUSED ? (size_t)in.pitch * a.M : 0, s, a, in);
 }
 
 // ---------------------------------------------------------------- M > 16: tcgen05
@@ -355,17 +427,22 @@ cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int
     return cudaGetLastError();
 }
 
-cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const int8_t* xq, const float* scale,
-                        int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc, cudaStream_t s) {
+cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x, bool rmsnorm,
+                        int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
+                        cudaStream_t s) {
     Int8Args a{Wq, wstep, xq, scale, residual, y16, y32, acc, (int)M, (int)N, (int)K};
-    if (M <= 8) return launch_gemv_nt<1>(a, s);
-    if (M <= 16) return launch_gemv_nt<2>(a, s);
+    const GemvIn in{x, rmsnorm ? 1 : 0, (int)K + 16};
+    if (M <= kFusedTokens && M * in.pitch <= kFusedBytes) return launch_gemv_nt<1, true>(a, in, s);
+    cudaError_t e = launch_act_quant(x, M, K, XQ_NATURAL, xq, scale, nullptr, s, rmsnorm);
+    if (e != cudaSuccess) return e;
+    if (M <= 8) return launch_gemv_nt<1, false>(a, in, s);
+    if (M <= 16) return launch_gemv_nt<2, false>(a, in, s);
     CUtensorMap mapA, mapB;
     if (!make_map(&mapA, xq, (uint64_t)M, (uint64_t)K, BM, BK, true) ||
         !make_map(&mapB, Wq, (uint64_t)N, (uint64_t)K, BN, BK, true))
         return cudaErrorInvalidValue;
     unsigned* err = nullptr;
-    cudaError_t e = device_error_word(&err);
+    e = device_error_word(&err);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     e = cudaGetDevice(&dev);

@@ -173,8 +173,10 @@ size_t kv4_tile_workspace_bytes(int D);
 
 // ---- 8-bit linear layers (int8.cu); one of y16, y32 is set
 cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int8_t* Wq, float* wstep, cudaStream_t s);
-cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const int8_t* xq, const float* scale,
-                        int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc, cudaStream_t s);
+// quantises x (xq [M, K], scale [M]: scratch), then the product
+cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x, bool rmsnorm,
+                        int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
+                        cudaStream_t s);
 
 // ---- device error word: set by bounded waits inside kernels that give up.
 // Address of the current device's word (for kernels), and a host read that

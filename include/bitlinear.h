@@ -28,7 +28,7 @@
  *   - Kernels launch with programmatic dependent launch: a call's kernel may start
  *     while the previous kernel in the stream finishes, and waits for it before
  *     reading its inputs x / h or writing anything. The packed weights (Wp, Wg,
- *     Wu, Wd) are the exception: the streamed GEMV starts copying them before that
+ *     Wu, Wd, Wq) are the exception: the streamed GEMVs start copying them before that
  *     wait. So packed weights must not be written by the kernel just before the
  *     call in the same stream if that kernel triggers programmatic dependent launch
  *     early (the library's own kernels that do never write weights; the packing
