@@ -10,6 +10,6 @@ from .binding import (  # noqa: F401
     BL_OP_VALIDATE, LIB_PATH, SIGNATURES, STATUS_NAMES, BitLinearError, ffn, forward, forward_ex, forward_rowwise,
     gemv_kernel, get_device_error, lib, pack_weights, pack_weights_rowwise, quant_act, set_gemv_kernel,
     validate_packed, workspace_bytes, BL_OP_FFN_TP_UP, BL_OP_FFN_TP_DOWN, absmean_sum, pack_weights_global,
-    ffn_tp_up, ffn_tp_down, ffn_tp_finish, BL_OP_KV4_ATTENTION, forward_int8, pack_weights_int8,
+    ffn_tp_up, ffn_tp_down, ffn_tp_finish, BL_OP_FORWARD_INT8, BL_OP_KV4_ATTENTION, forward_int8, pack_weights_int8,
 )
 from .kv4 import Kv4Cache, kv4_append, kv4_attention, kv4_cache, kv4_read  # noqa: F401

@@ -26,7 +26,7 @@ STATUS_NAMES = {
 }
 BL_BF16, BL_FP32 = 0, 1
 BL_OP_PACK, BL_OP_FORWARD, BL_OP_FFN, BL_OP_VALIDATE, BL_OP_FFN_TP_UP, BL_OP_FFN_TP_DOWN = 0, 1, 2, 3, 4, 5
-BL_OP_KV4_ATTENTION = 6
+BL_OP_KV4_ATTENTION, BL_OP_FORWARD_INT8 = 6, 7
 BL_GEMV_AUTO, BL_GEMV_STREAM, BL_GEMV_TENSOR, BL_GEMV_LUT = 0, 1, 2, 3
 
 # Every symbol include/bitlinear.h declares, with (restype, argtypes).
@@ -319,7 +319,7 @@ def forward_int8(Wq: torch.Tensor, wstep: torch.Tensor, x: torch.Tensor, rmsnorm
             out = (x if out_dtype is torch.bfloat16 else wstep).new_empty((M, N))
         acc = torch.empty((M, N), dtype=torch.int32, device=x.device) if want_acc else None
         if ws is None:
-            ws = Wq.new_empty(_forward_bytes(M, N, K))
+            ws = Wq.new_empty(_int8_bytes(M, N, K))
         st = lib().bitlinear_forward_int8(Wq.data_ptr(), wstep.data_ptr(), N, K, x.data_ptr(), M, 1 if rmsnorm else 0,
                                           None if residual is None else residual.data_ptr(), out.data_ptr(),
                                           BL_FP32 if out_dtype is torch.float32 else BL_BF16,
@@ -334,8 +334,8 @@ _HERE = nullcontext()
 
 
 @functools.lru_cache(maxsize=4096)
-def _forward_bytes(M: int, N: int, K: int) -> int:
-    return workspace_bytes(BL_OP_FORWARD, M, N, K)
+def _int8_bytes(M: int, N: int, K: int) -> int:
+    return workspace_bytes(BL_OP_FORWARD_INT8, M, N, K)
 
 
 def validate_packed(Wp: torch.Tensor) -> int:

@@ -114,6 +114,18 @@ inline size_t pack_ws(int64_t N, int64_t K) {
     return align_up((size_t)bl::absmean_blocks(N * K) * sizeof(double));
 }
 
+// 8-bit layer: codes and scales of x.
+struct Int8Ws {
+    size_t xq, scale, total;
+};
+inline Int8Ws int8_ws(int64_t M, int64_t K) {
+    Int8Ws w;
+    w.xq = 0;
+    w.scale = align_up((size_t)(M * K));
+    w.total = w.scale + align_up((size_t)M * 4);
+    return w;
+}
+
 // Device check: the kernels are built for sm_100a only.
 bl_status check_device() {
     static int cached[64];  // 0 unknown, 1 ok, 2 unsupported
@@ -238,6 +250,7 @@ BL_API size_t bitlinear_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         case BL_OP_VALIDATE: return kWsAlign;
         case BL_OP_FFN_TP_UP: return tp_up_ws(M, N, K).total;
         case BL_OP_FFN_TP_DOWN: return tp_down_ws(M, N, K).total;
+        case BL_OP_FORWARD_INT8: return int8_ws(M, K).total;
         case BL_OP_KV4_ATTENTION:
             return K == 64 || K == 128 ? align_up(bl::kv4_attention_workspace_bytes(std::min(M, kMaxM), std::min<int64_t>(N, 1024), (int)K)) : 0;
         default: return 0;
@@ -706,7 +719,7 @@ BL_API bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, in
     if (!aligned(Wq, 16) || !aligned(wstep, 4) || !aligned(x, 16) || !aligned(y, ydt == BL_FP32 ? 4 : 2) ||
         (residual && !aligned(residual, 2)) || (acc && !aligned(acc, 4)))
         return BL_ERR_ALIGN;
-    const ForwardWs w = forward_ws(M, N, K);
+    const Int8Ws w = int8_ws(M, K);
     if (bl_status st = check_ws(ws, ws_bytes, w.total)) return st;
     if (bl_status st = check_device()) return st;
     cudaStream_t s = (cudaStream_t)stream;

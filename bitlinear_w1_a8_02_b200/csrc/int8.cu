@@ -3,11 +3,11 @@
 //
 //   y[m, n] = [residual +] fl(fl(float(acc) wstep[n]) fl(1 / s_m))
 //
-// M <= 16 tokens: bound by the N K weight bytes. Warps stream 16 rows at a time
+// One token (and up to eight with short rows): bound by the N K weight bytes. Warps stream 16 rows at a time
 // from DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A): a
 // lane's 16 bytes of a row are the four words of two MMAs, and the lane's 16 bytes
-// of a token's codes line up with them, so neither side is rearranged. Up to four
-// tokens are quantised inside the kernel, by every block for itself.
+// of a token's codes line up with them, so neither side is rearranged. A single
+// token is quantised inside the kernel, by every block for itself.
 #include <algorithm>
 
 #include "common.cuh"
@@ -89,7 +89,9 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 
 constexpr int kGemvWarps = 8;
 constexpr int kUnroll = 5;               // 64-byte chunks of a row pair in flight per warp
-constexpr int kFusedTokens = 4;          // up to here the kernel quantises x itself
+constexpr int kGemvTokens = 8;           // most tokens of the GEMV,
+constexpr int kGemvMaxK = 4096;          // and the longest K with more than one (measured: at 6912 the clusters are faster)
+constexpr int kFusedTokens = 1;          // up to here the kernel quantises x itself
 constexpr int kFusedBytes = 40 * 1024;   // and keeps its codes in shared memory
 
 struct GemvIn {
@@ -101,10 +103,10 @@ struct GemvIn {
 // The kernel's blocks are persistent and take every gridDim.x-th tile of 16 rows; the 8 warps of a block share a
 // tile (64-byte chunks of K in turn), their sums meet in shared memory. The first tile's weights are under way before
 // the kernel waits for the one before it: weights are constants (the header says so for packed weights).
-template <int NT, bool FUSED>
-__global__ void __launch_bounds__(32 * kGemvWarps, NT == 1 ? 4 : 3) gemv_int8_kernel(const Int8Args a, const GemvIn in) {
-    __shared__ int part[2][kGemvWarps][NT * 4][32];
-    __shared__ float xstep_sh[8 * NT];
+template <bool FUSED>
+__global__ void __launch_bounds__(32 * kGemvWarps, 4) gemv_int8_kernel(const Int8Args a, const GemvIn in) {
+    __shared__ int part[2][kGemvWarps][4][32];
+    __shared__ float xstep_sh[8];
     __shared__ float fscratch[kGemvWarps];
     __shared__ double dscratch[kGemvWarps];
     extern __shared__ __align__(16) int8_t codes[];
@@ -173,52 +175,39 @@ __global__ void __launch_bounds__(32 * kGemvWarps, NT == 1 ? 4 : 3) gemv_int8_ke
     }
     __syncthreads();
 
-    const int8_t* x[NT];
-    bool live[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        live[nt] = nt * 8 + r < a.M;
-        const int m = min(nt * 8 + r, a.M - 1);
-        x[nt] = (FUSED ? codes + m * in.pitch : a.xq + (int64_t)m * a.K) + 16 * t;
-    }
+    const bool live = r < a.M;
+    const int8_t* x = (FUSED ? codes + min(r, a.M - 1) * in.pitch : a.xq + (int64_t)min(r, a.M - 1) * a.K) + 16 * t;
     int turn = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
-        // the output this thread stores after the sums have met: element e = warp of nt = 0 .. NT - 1
+        // the output this thread stores after the sums have met: accumulator element `warp` of its lane
         const int n = tile * 16 + r + 8 * ((warp & 3) >> 1);
-        const float ws = warp < 4 * NT && n < a.N ? a.wstep[n] : 0.0f;
-        int d[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0;
+        const float ws = warp < 4 && n < a.N ? a.wstep[n] : 0.0f;
+        int d[4] = {0, 0, 0, 0};
         for (int c = warp; c < n_chunks; c += kGemvWarps * kUnroll) {
             if (c != warp || tile != blockIdx.x) load(tile, c);
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
                 const int k = (c + i * kGemvWarps) * 64;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 b = k + 16 * t < a.K && live[nt] ? *reinterpret_cast<const uint4*>(x[nt] + k) : zero;
-                    mma_s8(d[nt], u[i].x, v[i].x, u[i].y, v[i].y, b.x, b.y);
-                    mma_s8(d[nt], u[i].z, v[i].z, u[i].w, v[i].w, b.z, b.w);
-                }
+                const uint4 b = k + 16 * t < a.K && live ? *reinterpret_cast<const uint4*>(x + k) : zero;
+                mma_s8(d, u[i].x, v[i].x, u[i].y, v[i].y, b.x, b.y);
+                mma_s8(d, u[i].z, v[i].z, u[i].w, v[i].w, b.z, b.w);
             }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[turn][warp][nt * 4 + e][lane] = d[nt][e];
+        for (int e = 0; e < 4; ++e) part[turn][warp][e][lane] = d[e];
         __syncthreads();  // the other half of `part` is free: every warp has passed the tile before
-        if (warp < 4 * NT) {
+        if (warp < 4) {
             int acc = 0;
 #pragma unroll
             for (int w = 0; w < kGemvWarps; ++w) acc += part[turn][w][warp][lane];
-            const int m = (warp >> 2) * 8 + 2 * t + (warp & 1);
+            const int m = 2 * t + (warp & 1);
             if (n < a.N && m < a.M) store_one(a, m, n, acc, ws, xstep_sh[m]);
         }
     }
 }
 
-template <int NT, bool FUSED>
-cudaError_t launch_gemv_nt(const Int8Args& a, const GemvIn& in, cudaStream_t s) {
+template <bool FUSED>
+cudaError_t launch_gemv(const Int8Args& a, const GemvIn& in, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -227,32 +216,43 @@ cudaError_t launch_gemv_nt(const Int8Args& a, const GemvIn& in, cudaStream_t s) 
         int sms = 0, per = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, gemv_int8_kernel<NT, FUSED>, 32 * kGemvWarps, FUSED ? 8192 : 0);
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, gemv_int8_kernel<FUSED>, 32 * kGemvWarps, FUSED ? 8192 : 0);
         if (e != cudaSuccess) return e;
         if (dev < 64) resident[dev] = sms * per;
     }
     const int tiles = (a.N + 15) / 16;
     const int grid = std::min(tiles, dev < 64 ? resident[dev] : 148);
-    return launch_pdl(gemv_int8_kernel<NT, FUSED>, dim3((unsigned)grid), dim3(32 * kGemvWarps),
+    return launch_pdl(gemv_int8_kernel<FUSED>, dim3((unsigned)grid), dim3(32 * kGemvWarps),
                       FUSED ? (size_t)in.pitch * a.M : 0, s, a, in);
 }
 
 // ---------------------------------------------------------------- M > 16: tcgen05
-constexpr int BM = 128, BN = 256, BK = 128;
-constexpr int STAGES = 4;
-constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
+//
+// M > 128: TMA brings 128 bytes of K of 128 tokens and BN weight rows per stage, one thread issues tcgen05.mma kind::i8
+// into one of two int32 accumulators in TMEM, four warps read the other one out. Persistent blocks take whole tiles;
+// weight tiles are shared by consecutive tiles.
+constexpr int BM = 128, BK = 128;
+constexpr int A_BYTES = BM * BK;
 constexpr int EPI_WARPS = 4;
 constexpr int GEMM_THREADS = 64 + 32 * EPI_WARPS;
-constexpr size_t GEMM_SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + (2 * STAGES + 4) * 8;
+template <int BN>
+struct Gemm {
+    static constexpr int B_BYTES = BN * BK;
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int BARS = 2 * STAGES + 4;
+    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + BARS * 8;
+};
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
 __host__ __device__ constexpr uint32_t idesc_s8s8(int m, int n) {
     return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+template <int BN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     gemm_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Int8Args a,
                      unsigned* err) {
+    constexpr int STAGES = Gemm<BN>::STAGES, B_BYTES = Gemm<BN>::B_BYTES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
@@ -417,6 +417,216 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
 }
 
+// ---------------------------------------------------------------- up to 128 tokens: tcgen05, weights as A
+//
+// Bound by the weights' bytes, so every SM has to stream its share: a block takes 128 weight rows (the MMA's M) and the
+// tokens are its N, and where there are fewer tiles of 128 rows than SMs, the blocks of a cluster take a K range of one
+// tile each. Their int32 sums meet through distributed shared memory: each block finishes its share of the rows.
+// Weight loads start before the kernel waits for the one before it.
+constexpr int FEW_MAX = 128;
+constexpr int FEW_SMEM = 104 * 1024;  // two blocks per SM
+constexpr int FEW_STAGES_MAX = 6;
+
+struct FewArgs {
+    int stages, cols, log_split;  // ring stages, tokens rounded up to 16, log2 of the blocks per tile
+};
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(GEMM_THREADS)
+    few_int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Args a,
+                    const FewArgs f, unsigned* err) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * FEW_STAGES_MAX + 1];
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    __shared__ float xstep_sh[FEW_MAX];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int x_bytes = f.cols * BK, stage_bytes = A_BYTES + x_bytes;
+    auto full = [&](int i) { return tc::smem_u32(bars + i); };
+    auto empty = [&](int i) { return tc::smem_u32(bars + FEW_STAGES_MAX + i); };
+    const uint32_t done = tc::smem_u32(bars + 2 * FEW_STAGES_MAX);
+    volatile int* aborted = &abort_sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x & ((1 << f.log_split) - 1), n0 = (int)(blockIdx.x >> f.log_split) * BM;
+    const int nkb = (a.K + BK - 1) / BK;
+    const int kb0 = nkb * rank >> f.log_split, kb1 = nkb * (rank + 1) >> f.log_split;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < f.stages; ++i) tc::mbar_init(full(i), 1), tc::mbar_init(empty(i), 1);
+        tc::mbar_init(done, 1);
+        abort_sh = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tc::smem_u32(&tmem_base_sh), 128);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base_sh;
+    auto give_up = [&]() {
+        atomicOr(err, 1u);
+        *aborted = 1;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            auto weights = [&](int kb, int s) {
+                tc::mbar_arrive_expect_tx(full(s), stage_bytes);
+                tc::tma_load_2d(tc::smem_u32(ring + s * stage_bytes), &tmW, kb * BK, n0, full(s));
+            };
+            auto tokens = [&](int kb, int s) {
+                tc::tma_load_2d(tc::smem_u32(ring + s * stage_bytes + A_BYTES), &tmX, kb * BK, 0, full(s));
+            };
+            const int ahead = min(f.stages, kb1 - kb0);
+            for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
+            grid_dependency_wait();
+            grid_dependents_launch();
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // codes written by the kernel before
+            for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
+            int g = ahead;
+            for (int kb = kb0 + ahead; kb < kb1 && !*aborted; ++kb, ++g) {
+                const int s = g % f.stages;
+                if (!tc::mbar_wait(empty(s), (g / f.stages - 1) & 1, WAIT_LIMIT_NS)) {
+                    give_up();
+                    break;
+                }
+                weights(kb, s);
+                tokens(kb, s);
+            }
+            if (*aborted)  // let the copies still in flight land before the block exits
+                for (int h = max(0, g - f.stages); h < g; ++h) tc::mbar_wait(full(h % f.stages), (h / f.stages) & 1, WAIT_LIMIT_NS);
+        }
+    } else if (warp == 1) {
+        grid_dependency_wait();
+        if (lane == 0) {
+            const uint32_t idesc = idesc_s8s8(BM, 16) - (2u << 17) + (static_cast<uint32_t>(f.cols >> 3) << 17);
+            bool ok = true;
+            for (int g = 0; g < kb1 - kb0; ++g) {
+                const int s = g % f.stages;
+                ok = !*aborted && tc::mbar_wait(full(s), (g / f.stages) & 1, WAIT_LIMIT_NS);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint64_t wd = tc::desc_kmajor_sw128(tc::smem_u32(ring + s * stage_bytes));
+                const uint64_t xd = tc::desc_kmajor_sw128(tc::smem_u32(ring + s * stage_bytes + A_BYTES));
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk) tc::mma_i8(tmem, wd + 2 * kk, xd + 2 * kk, idesc, g != 0 || kk != 0);
+                tc::mma_commit(empty(s));
+            }
+            if (!ok) give_up();
+            tc::mma_commit(done);
+        }
+        __syncwarp();
+    } else {
+        grid_dependency_wait();
+        const int m = threadIdx.x - 64;
+        if (m < a.M) xstep_sh[m] = __fdiv_rn(1.0f, a.scale[m]);
+    }
+    // the sums -> shared memory [token][weight row] (the ring is no longer in use)
+    const bool ok = tc::mbar_wait(done, 0, 2 * WAIT_LIMIT_NS) && !*aborted;
+    if (!__all_sync(0xffffffffu, ok)) give_up();
+    tc::fence_after_sync();
+    int* sums = reinterpret_cast<int*>(ring);
+    if (warp >= 2 && !*aborted) {
+        const int q = warp & 3;  // the TMEM lane quarter this warp may read
+        for (int c = 0; c < f.cols; c += 16) {
+            uint32_t v[16];
+            tc::tmem_ld_32x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sums[(c + j) * BM + q * 32 + lane] = (int)v[j];
+        }
+    }
+    tc::fence_before_sync();
+    if (f.log_split)
+        tc::cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= 2 && !*aborted) {
+        // this block finishes rows rank * rows .. of the tile; a thread keeps its row
+        const int rows = BM >> f.log_split, et = threadIdx.x - 64;
+        const int row = rank * rows + (et & (rows - 1)), n = n0 + row;
+        if (n < a.N) {
+            const float ws = a.wstep[n];
+            for (int m = et / rows; m < a.M; m += 1 << f.log_split) {
+                int acc = sums[m * BM + row];
+                if (f.log_split) {
+                    const uint32_t at = tc::smem_u32(sums + m * BM + row);
+                    acc = 0;
+                    for (int p = 0; p < 1 << f.log_split; ++p) acc += ld_cluster(tc::map_to_rank(at, p));
+                }
+                store_one(a, m, n, acc, ws, xstep_sh[m]);
+            }
+        }
+    }
+    if (f.log_split)
+        tc::cluster_sync();  // the others have read this block's sums
+    else
+        __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, 128);
+}
+
+cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
+    FewArgs f;
+    f.cols = (a.M + 15) / 16 * 16;
+    f.stages = std::min(FEW_STAGES_MAX, (FEW_SMEM - 1024) / (A_BYTES + f.cols * BK));
+    const int tiles = (a.N + BM - 1) / BM, nkb = (a.K + BK - 1) / BK;
+    f.log_split = 0;  // up to two blocks per SM and 8 per cluster, at least two k-blocks each
+    while (f.log_split < 3 && (tiles << (f.log_split + 1)) <= 2 * sms && nkb >= 4 << f.log_split) ++f.log_split;
+    CUtensorMap mapW, mapX;
+    if (!make_map(&mapW, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BM, BK, true) ||
+        !make_map(&mapX, a.xq, (uint64_t)a.M, (uint64_t)a.K, (uint32_t)f.cols, BK, true))
+        return cudaErrorInvalidValue;
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    static bool attr_set[64];
+    if (dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(few_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles << f.log_split));
+    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.dynamicSmemBytes = (size_t)1024 + f.stages * (A_BYTES + f.cols * BK);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << f.log_split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, few_int8_kernel, mapW, mapX, a, f, err);
+}
+
+template <int BN>
+cudaError_t launch_gemm_bn(const Int8Args& a, int sms, int dev, cudaStream_t s) {
+    CUtensorMap mapA, mapB;
+    if (!make_map(&mapA, a.xq, (uint64_t)a.M, (uint64_t)a.K, BM, BK, true) ||
+        !make_map(&mapB, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BN, BK, true))
+        return cudaErrorInvalidValue;
+    unsigned* err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    static bool attr_set[64];
+    if (dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(gemm_int8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Gemm<BN>::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev] = true;
+    }
+    const int64_t tiles = (int64_t)((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM);
+    return launch_pdl(gemm_int8_kernel<BN>, dim3((unsigned)std::min<int64_t>(tiles, sms)), dim3(GEMM_THREADS), Gemm<BN>::SMEM, s,
+                      mapA, mapB, a, err);
+}
+
 }  // namespace
 
 cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int8_t* Wq, float* wstep, cudaStream_t s) {
@@ -427,31 +637,47 @@ cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int
     return cudaGetLastError();
 }
 
+namespace {
+// 256 weight rows a tile unless narrower ones finish sooner: waves times the relative time of a tile.
+int int8_tile_width(int64_t M, int64_t N, int sms) {
+    const int64_t mt = (M + BM - 1) / BM;
+    const int width[3] = {256, 128, 64};
+    const double cost[3] = {1.0, 0.68, 0.59};
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < 3; ++i) {
+        const double t = (double)((mt * ((N + width[i] - 1) / width[i]) + sms - 1) / sms) * cost[i];
+        if (i == 0 || t < least - 1e-9) best = i, least = t;
+    }
+    return width[best];
+}
+}  // namespace
+
 cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x, bool rmsnorm,
                         int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
                         cudaStream_t s) {
     Int8Args a{Wq, wstep, xq, scale, residual, y16, y32, acc, (int)M, (int)N, (int)K};
     const GemvIn in{x, rmsnorm ? 1 : 0, (int)K + 16};
-    if (M <= kFusedTokens && M * in.pitch <= kFusedBytes) return launch_gemv_nt<1, true>(a, in, s);
+    if (M <= kFusedTokens && M * in.pitch <= kFusedBytes) return launch_gemv<true>(a, in, s);
     cudaError_t e = launch_act_quant(x, M, K, XQ_NATURAL, xq, scale, nullptr, s, rmsnorm);
     if (e != cudaSuccess) return e;
-    if (M <= 8) return launch_gemv_nt<1, false>(a, in, s);
-    if (M <= 16) return launch_gemv_nt<2, false>(a, in, s);
-    CUtensorMap mapA, mapB;
-    if (!make_map(&mapA, xq, (uint64_t)M, (uint64_t)K, BM, BK, true) ||
-        !make_map(&mapB, Wq, (uint64_t)N, (uint64_t)K, BN, BK, true))
-        return cudaErrorInvalidValue;
-    unsigned* err = nullptr;
-    e = device_error_word(&err);
-    if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
+    if (M <= kGemvTokens && K <= kGemvMaxK) return launch_gemv<false>(a, in, s);
+    int dev = 0;
     e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GEMM_SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((N + BN - 1) / BN) * ((M + BM - 1) / BM);
-    return launch_pdl(gemm_int8_kernel, dim3((unsigned)std::min<int64_t>(tiles, sms)), dim3(GEMM_THREADS), GEMM_SMEM, s, mapA,
-                      mapB, a, err);
+    static int num_sms[64];
+    int sms = dev < 64 ? num_sms[dev] : 0;
+    if (!sms) {
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) num_sms[dev] = sms;
+    }
+    if (M <= FEW_MAX) return launch_few(a, sms, dev, s);
+    switch (int8_tile_width(M, N, sms)) {
+        case 64: return launch_gemm_bn<64>(a, sms, dev, s);
+        case 128: return launch_gemm_bn<128>(a, sms, dev, s);
+        default: return launch_gemm_bn<256>(a, sms, dev, s);
+    }
 }
 
 }  // namespace bl

@@ -86,7 +86,8 @@ typedef enum {
     BL_OP_VALIDATE = 3, /* sizes ignored */
     BL_OP_FFN_TP_UP = 4,    /* sizes: M, N = f_local (the rank's hidden columns), K = d */
     BL_OP_FFN_TP_DOWN = 5,  /* sizes: M, N = d, K = f_local */
-    BL_OP_KV4_ATTENTION = 6 /* sizes: M = max_q, N = Hq / Hkv, K = D */
+    BL_OP_KV4_ATTENTION = 6, /* sizes: M = max_q, N = Hq / Hkv, K = D */
+    BL_OP_FORWARD_INT8 = 7  /* sizes: M, N, K */
 } bl_op;
 
 /* Kernels for M <= 16 tokens (bitlinear_set_gemv_kernel). */
@@ -491,7 +492,7 @@ bl_status bitlinear_pack_weights_int8(const void* W, int wdt, int64_t N, int64_t
  *   x         [M, K] device bf16, 16-byte aligned; 0 <= M <= 65535
  *   residual  [M, N] device bf16, may be NULL; acc [M, N] device int32, may be NULL
  *   y         [M, N], contiguous
- *   ws        bitlinear_workspace_bytes(BL_OP_FORWARD, M, N, K) bytes
+ *   ws        bitlinear_workspace_bytes(BL_OP_FORWARD_INT8, M, N, K) bytes
  */
 bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x,
                                  int64_t M, int32_t rmsnorm, const uint16_t* residual, void* y, int ydt,

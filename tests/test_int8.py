@@ -47,7 +47,7 @@ def test_refusals():
     assert pk(P(A), 0, 8, 16, None, P(A), None) == NULL
     assert pk(P(A + 8), 0, 8, 16, P(A), P(A), None) == ALIGN
     assert pk(P(A), 0, 8, 16, P(A + 4), P(A), None) == ALIGN
-    need = L.bitlinear_workspace_bytes(bl.BL_OP_FORWARD, 2, 8, 32)
+    need = L.bitlinear_workspace_bytes(bl.BL_OP_FORWARD_INT8, 2, 8, 32)
 
     def fw(**kw):
         a = dict(Wq=A, ws_=A, N=8, K=32, x=A, M=2, rms=0, res=None, y=A, ydt=0, acc=None, ws=A, wsb=need)
@@ -86,11 +86,11 @@ def test_pack(N, K, dtype):
     assert np.array_equal(np_(Wq), rq) and np.array_equal(np_(step), rs)
 
 
-SHAPES = [(1, 16), (17, 48), (257, 80), (640, 2560), (2560, 2560), (1000, 6912), (19001, 256), (31, 28672)]
+SHAPES = [(1, 16), (17, 48), (257, 80), (640, 2560), (2560, 2560), (1000, 6912), (19001, 256), (31, 28672), (5000, 4000)]
 
 
 @gpu
-@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 64, 129, 300])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 64, 128, 129, 300])
 @pytest.mark.parametrize("N,K", SHAPES)
 def test_forward(M, N, K):
     W = synth.weights(N, K, 0.02, seed=3)
