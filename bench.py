@@ -513,9 +513,9 @@ def run_extras(args, bl, synth, dev, hbm_peak, int8_peak):
 
     # Every BitLinear of a 2B-shaped decoder layer, 30 layers, one token per step:
     # Q/K/V in one call with the block's pre-norm, the output projection with its
-    # subln and the residual, then the FFN. The attention itself (RoPE, softmax,
-    # the KV cache) is not part of this library: the output projection reads a
-    # fixed synthetic attention output.
+    # subln and the residual, then the FFN. The attention itself (kv4_append,
+    # kv4_attention) is not part of this measurement: the output projection reads
+    # a fixed synthetic attention output.
     qkv_rows = [2560, 640, 640]
     dec = []
     for layer in range(LAYERS):
