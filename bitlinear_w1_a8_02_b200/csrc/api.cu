@@ -680,6 +680,9 @@ BL_API bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, in
     bl::Kv4Seqs seqs;
     if (bl_status st = kv4_args(cache, batch, M, &view, &seqs)) return st;
     if (!heads_ok(Hq, cache->kv_heads) || max_q < 0 || !(scale > 0.0f && scale <= 3.0e38f)) return BL_ERR_SHAPE;
+    // units of work (blocks of keys x items of rows) are counted in 32 bits
+    const int64_t room = (int64_t)batch->W * cache->page_size;
+    if ((M * Hq / 256 + (int64_t)batch->S * cache->kv_heads) * (room / 128 + 8) >= (int64_t)1 << 31) return BL_ERR_SHAPE;
     if (M == 0) return BL_OK;
     const int64_t D = cache->head_dim;
     if (bl_status st = rows_ok(q, q_stride, Hq * D)) return st;

@@ -92,7 +92,7 @@ constexpr int kUnroll = 5;               // 64-byte chunks of a row pair in flig
 constexpr int kGemvTokens = 8;           // most tokens of the GEMV,
 constexpr int kGemvMaxK = 4096;          // and the longest K with more than one (measured: at 6912 the clusters are faster)
 constexpr int kFusedTokens = 1;          // up to here the kernel quantises x itself
-constexpr int kFusedBytes = 40 * 1024;   // and keeps its codes in shared memory
+constexpr int kFusedBytes = 32 * 1024;   // and keeps its codes in shared memory (48 KiB with the static part)
 
 struct GemvIn {
     const uint16_t* x;  // fused: activations to quantise

@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             const bool whole = starts && ends;
             const int64_t row = row_out;
             const size_t slot_at = (size_t)(2 * c + (starts ? 1 : 0)) * C::SLOT;
+            const bool piece_sees = limit > b0 * BLK;
             if (ok) {
                 have = fetch();
                 ok = !*aborted && tc::mbar_wait(ofull(i), no & 1, WAIT_NS);
@@ -752,7 +753,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 break;
             }
             tc::fence_after_sync();
-            const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+            // no sum: no key in sight, or every score was -inf, which has no softmax
+            const float inv = den == 0.0f ? (piece_sees ? NAN : 0.0f) : 1.0f / den;
             float4* slot = reinterpret_cast<float4*>(a.slots + slot_at) + i * TM + r;
             // whole rows go out through the tile's query memory, which no MMA reads any more
             uint32_t ov[2][32];
@@ -792,7 +794,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 __syncwarp();  // the warp's own next queries go to the rows that it has just read
             } else {
                 float2* st = reinterpret_cast<float2*>(a.slots + slot_at + ROWS * D) + i * TM + r;
-                *st = make_float2(mx == -INFINITY ? -INFINITY : msc, den);
+                *st = make_float2(mx == -INFINITY ? -INFINITY : msc, den == 0.0f && piece_sees ? -0.0f : den);  // -0: as `inv` above
             }
         }
         if (tid == 0) a.joins[c] = ok ? join : make_int4(0, 0, 0, -1);
@@ -827,7 +829,12 @@ __global__ void __launch_bounds__(ROWS) kv4_tile_join_kernel(const TileArgs a) {
     const int pieces = j.w - c + 1;
     auto slot = [&](int p) { return a.slots + (size_t)(2 * (c + p) + (p == 0 ? 1 : 0)) * C::SLOT; };
     float m = -INFINITY;
-    for (int p = 0; p < pieces; ++p) m = fmaxf(m, slot(p)[ROWS * D + 2 * row]);
+    bool lost = false;  // a piece saw keys, but scores of -inf only
+    for (int p = 0; p < pieces; ++p) {
+        const float2 st = reinterpret_cast<const float2*>(slot(p) + ROWS * D)[row];
+        m = fmaxf(m, st.x);
+        lost |= st.y == 0.0f && signbit(st.y);
+    }
     float den = 0.0f;
     float4 v[4];
 #pragma unroll
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(ROWS) kv4_tile_join_kernel(const TileArgs a) {
             v[e].x += f * o.x, v[e].y += f * o.y, v[e].z += f * o.z, v[e].w += f * o.w;
         }
     }
-    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+    const float inv = den == 0.0f ? (lost ? NAN : 0.0f) : 1.0f / den;
     const int ri = t * ROWS + row;
     uint16_t* op = a.out + (int64_t)(j.x + ri / a.group) * a.out_stride + (j.y * a.group + ri % a.group) * D + 16 * blockIdx.y;
 #pragma unroll

@@ -111,6 +111,17 @@ def test_forward(M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("M", [1, 2])
+@pytest.mark.parametrize("K", [4080, 4096, 4112, 32752, 32768, 40928, 40944, 131072])
+def test_lengths_around_the_kernel_choice(M, K):
+    Wq = torch.randint(-127, 128, (35, K), dtype=torch.int8, device="cuda")
+    x = synth.activations(M, K, seed=1).cuda()
+    _, acc = bl.forward_int8(Wq, torch.ones(35, device="cuda"), x, want_acc=True)
+    codes, _, _ = bl.quant_act(x)
+    assert torch.equal(acc.double(), codes.double() @ Wq.double().t())
+
+
+@gpu
 @pytest.mark.parametrize("M", [3, 200])
 def test_extreme_codes(M):
     """Every code at its largest magnitude over the longest K of the checks: accumulators near 2^31."""

@@ -90,7 +90,7 @@ def test_refusals_rows():
                      (dict(cs=A + 4), ALIGN), (dict(max_pos=0), SHAPE), (dict(il=2), SHAPE), (dict(o_stride=2048), SHAPE)):
         assert _call("append", **kw) == want, kw
     for kw, want in ((dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("nan")), SHAPE),
-                     (dict(scale=float("inf")), SHAPE), (dict(max_q=-1), SHAPE), (dict(ws=None), NULL), (dict(ws=A + 16), ALIGN),
+                     (dict(scale=float("inf")), SHAPE), (dict(max_q=-1), SHAPE), (dict(M=65535, Hq=1024, q_stride=131072, o_stride=131072, W=1 << 18), SHAPE), (dict(ws=None), NULL), (dict(ws=A + 16), ALIGN),
                      (dict(wsb=1000), WS), (dict(max_q=3, Hq=16, q_stride=2048, o_stride=2048, wsb=binding.workspace_bytes(bl.BL_OP_KV4_ATTENTION, 1, 4, 128)), WS)):
         assert _call("attention", **kw) == want, kw
 
@@ -376,6 +376,27 @@ def test_marked_tokens_reach_only_rows_that_see_them(new):
     bl.kv4_append(qq, kk, vv, table(1, 128), *c.args())
     rk, rv = bl.kv4_read(*c.args(), 1)
     assert torch.isnan(rk).all() and (rv == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 90])
+def test_queries_without_a_softmax(new):
+    """A NaN or infinite query makes its row NaN in its head, also where every score is -inf; others are as before."""
+    lens = [(new, 900 + new), (new, 40 + new)]
+    b = Batch(lens, 128, 8, 2, 32, seed=6)
+    n = sum(kv for _, kv in lens)
+    k = b.rng.standard_normal((n, 2, 128)).astype(np.float32)
+    k[:, :, 7] = 1.0 + np.abs(k[:, :, 7])  # one sign: an infinite query there has scores of one sign
+    b.fill(k, b.rng.standard_normal((n, 2, 128)).astype(np.float32))
+    q = torch.from_numpy(b.rng.standard_normal((b.M, 8, 128))).to(torch.bfloat16).cuda()
+    want = np_(bl.kv4_attention(q, *b.args(), new).float())
+    q[0, 1, 7] = -float("inf")
+    q[new - 1, 5, 7] = float("inf")
+    q[2 * new - 1, 2, 100] = float("nan")
+    got = np_(bl.kv4_attention(q, *b.args(), new).float())
+    bad = np.zeros(got.shape[:2], bool)
+    bad[0, 1] = bad[new - 1, 5] = bad[2 * new - 1, 2] = True
+    assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], want[~bad])
 
 
 @gpu
