@@ -7,9 +7,7 @@ library is missing or fails to load, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -90,17 +88,27 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_native = None
+
+
+def native():
+    """The binding's compiled part, bound to the library (raises if either was not built)."""
+    global _native
+    if _native is None:
+        lib()
+        from . import _native as module
+
+        module.bind(LIB_PATH)
+        _native = module
+    return _native
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _raw_stream(index: int) -> int:
-    """Handle of the current stream of CUDA device `index`."""
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _check(st: int, where: str):
@@ -300,42 +308,12 @@ def forward_int8(Wq: torch.Tensor, wstep: torch.Tensor, x: torch.Tensor, rmsnorm
                  ws: Optional[torch.Tensor] = None):
     """One 8-bit linear layer of x [M, K] bf16 (after a unit-weight RMSNorm if asked): y [M, N] in out_dtype (bf16 or
     fp32), and the int32 accumulator with want_acc. Scratch is allocated per call unless `ws` is given."""
-    N, K = Wq.shape
-    M = x.shape[0]
-    index = x.get_device()
-    for t, name, dt, shape in ((Wq, "Wq", torch.int8, (N, K)), (wstep, "wstep", torch.float32, (N,)),
-                               (x, "x", torch.bfloat16, (M, K)), (residual, "residual", torch.bfloat16, (M, N)),
-                               (out, "out", None, (M, N))):
-        if t is not None and (t.dtype is not dt and dt is not None or t.shape != shape or t.get_device() != index or
-                              index < 0 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dt or 'bf16 or fp32'} CUDA tensor {shape} on the device of x, "
-                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if out is not None:
-        out_dtype = out.dtype
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("the output must be bf16 or fp32")
-    with _HERE if index == torch.cuda.current_device() else torch.cuda.device(index):
-        if out is None:
-            out = (x if out_dtype is torch.bfloat16 else wstep).new_empty((M, N))
-        acc = torch.empty((M, N), dtype=torch.int32, device=x.device) if want_acc else None
-        if ws is None:
-            ws = Wq.new_empty(_int8_bytes(M, N, K))
-        st = lib().bitlinear_forward_int8(Wq.data_ptr(), wstep.data_ptr(), N, K, x.data_ptr(), M, 1 if rmsnorm else 0,
-                                          None if residual is None else residual.data_ptr(), out.data_ptr(),
-                                          BL_FP32 if out_dtype is torch.float32 else BL_BF16,
-                                          None if acc is None else acc.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                          _raw_stream(index))
-    if st:
-        _check(st, "bitlinear_forward_int8")
-    return (out, acc) if want_acc else out
-
-
-_HERE = nullcontext()
-
-
-@functools.lru_cache(maxsize=4096)
-def _int8_bytes(M: int, N: int, K: int) -> int:
-    return workspace_bytes(BL_OP_FORWARD_INT8, M, N, K)
+    r = native().forward_int8(Wq, wstep, x, bool(rmsnorm), residual, bool(want_acc), out_dtype is torch.float32, out, ws)
+    if type(r) is int:
+        _check(r, "bitlinear_forward_int8")
+    return r
 
 
 def validate_packed(Wp: torch.Tensor) -> int:

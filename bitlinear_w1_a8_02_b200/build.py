@@ -1,4 +1,4 @@
-"""Build step of the CUDA library: nvcc for sm_100a, in-tree.
+"""Build step of the CUDA library (nvcc for sm_100a) and of the binding's native part (g++), in-tree.
 
 Compiles every ``csrc/*.cu`` to an object under ``_build/`` (in parallel, only
 when the source or a header changed) and links ``libbitlinear.so`` next to this
@@ -12,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -53,13 +54,39 @@ def _compile(src: str, verbose: bool) -> str:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        native = ex.submit(build_native)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        native.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([NVCC, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
     return LIB
+
+
+NATIVE = os.path.join(PKG, "_native.so")
+
+
+def build_native() -> str:
+    import torch
+
+    src = os.path.join(CSRC, "native.cpp")
+    header = os.path.join(INCLUDE, "bitlinear.h")
+    if os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return NATIVE
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", f"-isystem{at}/include", f"-isystem{cuda}/include", src, "-o", tmp,
+           f"-L{at}/lib", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on native.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 if __name__ == "__main__":

@@ -1,11 +1,13 @@
 """The 4-bit paged cache and the attention over it: codes, steps and rotated queries bit for bit
 against the definition, attention against 64 bits, refusals on the host."""
+import struct
+
 import numpy as np
 import pytest
 import torch
 
 import bitlinear_w1_a8_02_b200 as bl
-from bitlinear_w1_a8_02_b200 import binding, kv4
+from bitlinear_w1_a8_02_b200 import binding
 from tests import kv4_reference as ref
 from tests.gpu_util import np_
 
@@ -54,8 +56,8 @@ def _call(fn, **kw):
              cache=True, batch=True)
     for k, v in kw.items():
         next(d for d in (c, b, a) if k in d)[k] = v
-    C = kv4._pack_cache(*[x or 0 for x in c.values()], 0) if a["cache"] else None
-    B = kv4._pack_batch(*[x or 0 for x in b.values()]) if a["batch"] else None
+    C = struct.pack("=QQQQqiiii", *[x or 0 for x in c.values()], 0) if a["cache"] else None  # bl_kv4_cache
+    B = struct.pack("=QQQqii", *[x or 0 for x in b.values()]) if a["batch"] else None        # bl_kv4_batch
     L = bl.lib()
     if fn == "append":
         return L.bitlinear_kv4_append(a["q"], a["q_stride"], a["k"], a["k_stride"], a["v"], a["v_stride"], a["M"], a["Hq"],
