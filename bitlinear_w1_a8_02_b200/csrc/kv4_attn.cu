@@ -8,9 +8,9 @@
 // group, at most 8 NT) are the n of mma.sync m16n8k16:
 //   scores   S^T [16 keys x rows] = K [16 x D] Q^T: a thread's 16 bytes of a key
 //            hold an octet of each group, so each pair of k-steps stays inside one
-//            group. The nibbles enter as 128 + n (one shift and one AND/OR a pair);
-//            the accumulator starts at -136 sum q, which leaves sum c q exactly up
-//            to fp32 rounding, and the step multiplies once per key and group.
+//            group. The nibbles enter as bf16 subnormals (an AND and half a shift a
+//            pair, see raw_pair); the accumulator starts at -8 sum q, which leaves
+//            sum c q, and the step multiplies once per key and group.
 //   values   O^T [D x rows] += V^T [D x 16 keys] P^T: pairs of keys are brought
 //            together by byte permutes of the packed words, then one AND/OR and one
 //            multiply-add give the bf16 pair exactly (see kv4.cuh); P^T comes from the
@@ -108,10 +108,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
+// Nibbles I, I + 4 of a word as a bf16 pair without any arithmetic: a bf16's low 8 bits are linear (the subnormals and
+// the first normal binade have one spacing), so bits 0..3 are n 2^-133 and bits 4..7 16 n 2^-133; the tensor cores take
+// subnormals. Odd I come out 16 times as large, which the queries make up for.
 template <int I>
-__device__ __forceinline__ uint32_t raw_pair(uint32_t w) {  // nibbles I, I + 4 as 128 + n
-    return and_or(I == 0 ? w : w >> (4 * I), 0x000F000Fu, 0x43004300u);
+__device__ __forceinline__ uint32_t raw_pair(uint32_t w) {
+    const uint32_t x = I < 2 ? w : w >> 8;
+    return x & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
+
+constexpr int kSpacing = 133;  // -log2 of the spacing of bf16's subnormals
 
 // Units of kKeys keys of sequence s (0 when it has no new tokens or was refused).
 struct SeqWork {
@@ -294,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 
     // ---------------------------------------------------------------- consumers
     const int r = lane >> 2, t = lane & 3;
-    const float sc = a.scale_log2;
+    const int kr = r ^ ((r >> 1) & 1);  // key of score row r: neighbours in one order or the other, so that the keys a value
+                                        // load takes for t = 0 .. 3 are even and odd ones (two bank halves)
     int g = 0;
     int4 join = make_int4(0, 0, 0, -1);
     for (int u = u0; u < u1;) {
@@ -305,9 +312,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         const int rows = min(RB, it.w.n_q * a.group - it.rb * RB);
         const int begin = u;
 
-        // queries of this lane's rows (columns r of each n-tile) in the order of the nibbles, and -136 sum q
+        // Queries of this lane's rows (columns r of each n-tile) in the order of the nibbles, scaled by a power of two
+        // per row that brings the largest to 2^100 .. 2^101 (exact: products with n 2^-133 stay far from fp32's ends),
+        // and -8 sum q, which the accumulators of a group start from: they end as sum c q.
         uint32_t qf[NT][G][4];
         float c0[NT][G][4];
+        float sc[NT][2];  // of accumulator columns 2t, 2t + 1: softmax scale * log2(e), the rows' scaling taken back
         int lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -315,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             const int ri = it.rb * RB + row;
             const bool live = row < rows;
             const uint16_t* qp = a.q + (live ? (int64_t)(it.w.row0 + ri / a.group) * a.q_stride + (it.head * a.group + ri % a.group) * D : 0);
+            uint32_t top = 0;
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 uint4 x = make_uint4(0, 0, 0, 0);
@@ -323,16 +334,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 qf[nt][gr][1] = __byte_perm(x.x, x.z, 0x7632);
                 qf[nt][gr][2] = __byte_perm(x.y, x.w, 0x5410);
                 qf[nt][gr][3] = __byte_perm(x.y, x.w, 0x7632);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = __vmaxu2(top, qf[nt][gr][i] & 0x7FFF7FFFu);
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int shift = min(127, max(10, 227 - (int)(top >> 7)));
+            const uint32_t even = (uint32_t)(127 + shift) << 7, odd = (uint32_t)(123 + shift) << 7;
+            const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
                     sum += __uint_as_float(qf[nt][gr][i] << 16) + __uint_as_float(qf[nt][gr][i] & 0xffff0000u);
+                    const uint32_t f = i & 1 ? odd : even;
+                    qf[nt][gr][i] = bf16x2_mul(qf[nt][gr][i], f | f << 16);
+                }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                c0[nt][gr][0] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t);
-                c0[nt][gr][1] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                sum = sum * up * -0x1p-65f * 0x1p-65f;  // -8 * 2^-133
+                c0[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+                c0[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
                 c0[nt][gr][2] = c0[nt][gr][0], c0[nt][gr][3] = c0[nt][gr][1];
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sc[nt][e] = a.scale_log2 * __uint_as_float((uint32_t)(127 + kSpacing - __shfl_sync(0xffffffffu, shift, 8 * t + 4 * e)) << 23);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rc = it.rb * RB + nt * 8 + 2 * t + e;  // row of accumulator column e
@@ -369,31 +398,31 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             const uint16_t* ks = reinterpret_cast<const uint16_t*>(ring + st * St::BYTES + 2 * St::CODES) + at * G;
             const uint16_t* vs = ks + St::STEPS / 2;
 
-            // ---- scores of keys key0 + r and key0 + r + 8
+            // ---- scores of keys key0 + kr and key0 + kr + 8
             uint32_t ka[G], kb[G];
             float sa[G], sb[G];
             if constexpr (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4*>(kc + r * VB + 16 * t);
-                const uint4 y = *reinterpret_cast<const uint4*>(kc + (r + 8) * VB + 16 * t);
+                const uint4 x = *reinterpret_cast<const uint4*>(kc + kr * VB + 16 * t);
+                const uint4 y = *reinterpret_cast<const uint4*>(kc + (kr + 8) * VB + 16 * t);
                 ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
                 kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
-                const uint2 p = *reinterpret_cast<const uint2*>(ks + r * G);
-                const uint2 q = *reinterpret_cast<const uint2*>(ks + (r + 8) * G);
+                const uint2 p = *reinterpret_cast<const uint2*>(ks + kr * G);
+                const uint2 q = *reinterpret_cast<const uint2*>(ks + (kr + 8) * G);
                 sa[0] = __uint_as_float(p.x << 16), sa[1] = __uint_as_float(p.x & 0xffff0000u);
                 sa[2] = __uint_as_float(p.y << 16), sa[3] = __uint_as_float(p.y & 0xffff0000u);
                 sb[0] = __uint_as_float(q.x << 16), sb[1] = __uint_as_float(q.x & 0xffff0000u);
                 sb[2] = __uint_as_float(q.y << 16), sb[3] = __uint_as_float(q.y & 0xffff0000u);
             } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(kc + r * VB + 8 * t);
-                const uint2 y = *reinterpret_cast<const uint2*>(kc + (r + 8) * VB + 8 * t);
+                const uint2 x = *reinterpret_cast<const uint2*>(kc + kr * VB + 8 * t);
+                const uint2 y = *reinterpret_cast<const uint2*>(kc + (kr + 8) * VB + 8 * t);
                 ka[0] = x.x, ka[1] = x.y;
                 kb[0] = y.x, kb[1] = y.y;
-                const uint32_t p = *reinterpret_cast<const uint32_t*>(ks + r * G);
-                const uint32_t q = *reinterpret_cast<const uint32_t*>(ks + (r + 8) * G);
+                const uint32_t p = *reinterpret_cast<const uint32_t*>(ks + kr * G);
+                const uint32_t q = *reinterpret_cast<const uint32_t*>(ks + (kr + 8) * G);
                 sa[0] = __uint_as_float(p << 16), sa[1] = __uint_as_float(p & 0xffff0000u);
                 sb[0] = __uint_as_float(q << 16), sb[1] = __uint_as_float(q & 0xffff0000u);
             }
-            float sv[NT][4];  // (key r, col 0), (key r, col 1), (key r + 8, col 0), (key r + 8, col 1)
+            float sv[NT][4];  // (key kr, col 0), (key kr, col 1), (key kr + 8, col 0), (key kr + 8, col 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) sv[nt][0] = sv[nt][1] = sv[nt][2] = sv[nt][3] = 0.0f;
 #pragma unroll
@@ -417,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (key0 + r >= lim[nt][e]) sv[nt][e] = -INFINITY;
-                        if (key0 + r + 8 >= lim[nt][e]) sv[nt][2 + e] = -INFINITY;
+                        if (key0 + kr >= lim[nt][e]) sv[nt][e] = -INFINITY;
+                        if (key0 + kr + 8 >= lim[nt][e]) sv[nt][2 + e] = -INFINITY;
                     }
             }
             // ---- maximum, raised rarely
@@ -437,11 +466,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                         m = fmaxf(m, mx[nt][e]);
-                        const float now = m == -INFINITY ? 0.0f : m * sc;
+                        const float now = m == -INFINITY ? 0.0f : m * sc[nt][e];
                         const float f = exp2_approx(mx[nt][e] == -INFINITY ? -INFINITY : msc[nt][e] - now);
                         mx[nt][e] = m;
                         msc[nt][e] = now;
-                        thr[nt][e] = m + kRaise / sc;
+                        thr[nt][e] = m + kRaise / sc[nt][e];
                         den[nt][e] *= f;
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
@@ -455,30 +484,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(fmaf(sv[nt][e], sc, -msc[nt][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(fmaf(sv[nt][e], sc[nt][e & 1], -msc[nt][e & 1]));
                 den[nt][0] += p[0] + p[2];
                 den[nt][1] += p[1] + p[3];
                 pf[nt][0] = transpose8x8(pack_bf16(p[0], p[1]));
                 pf[nt][1] = transpose8x8(pack_bf16(p[2], p[3]));
             }
 
-            // ---- values: keys 2t, 2t + 1 (pair 0) and 2t + 8, 2t + 9 (pair 1)
+            // ---- values: score rows 2t, 2t + 1 (pair 0) and 2t + 8, 2t + 9 (pair 1)
             uint32_t s16[2][2], s24[2][2];  // [key pair][word]
             uint32_t xw[2][2][2];           // [key pair][word][nibbles 0-3 / 4-7]: the two keys' halves
 #pragma unroll
             for (int kp = 0; kp < 2; ++kp) {
-                const int k0 = 2 * t + 8 * kp;
+                const int k0 = 2 * t + (t & 1) + 8 * kp, k1 = 2 * t + 1 - (t & 1) + 8 * kp;  // the keys of these rows
                 uint32_t st0, st1;  // steps of the two keys for this lane's words
                 if constexpr (D == 128) {
                     st0 = *reinterpret_cast<const uint32_t*>(vs + k0 * G + ((2 * r) & 3));
-                    st1 = *reinterpret_cast<const uint32_t*>(vs + (k0 + 1) * G + ((2 * r) & 3));
+                    st1 = *reinterpret_cast<const uint32_t*>(vs + k1 * G + ((2 * r) & 3));
                 } else {
                     st0 = vs[k0 * G + (r & 1)];
-                    st1 = vs[(k0 + 1) * G + (r & 1)];
+                    st1 = vs[k1 * G + (r & 1)];
                 }
                 if (tail) {  // steps behind the last token are whatever the page holds
                     if (key0 + k0 >= it.w.len) st0 = 0;
-                    if (key0 + k0 + 1 >= it.w.len) st1 = 0;
+                    if (key0 + k1 >= it.w.len) st1 = 0;
                 }
                 const uint32_t lo = __byte_perm(st0, st1, 0x5410);
                 s16[kp][0] = bf16x2_mul(lo, kBf16x2Sixteen);
@@ -488,14 +517,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                     s16[kp][1] = bf16x2_mul(hi, kBf16x2Sixteen);
                     s24[kp][1] = bf16x2_mul(hi, kBf16x2MinusTwentyFour);
                     const uint2 x = *reinterpret_cast<const uint2*>(vc + k0 * VB + 8 * r);
-                    const uint2 y = *reinterpret_cast<const uint2*>(vc + (k0 + 1) * VB + 8 * r);
+                    const uint2 y = *reinterpret_cast<const uint2*>(vc + k1 * VB + 8 * r);
                     xw[kp][0][0] = __byte_perm(x.x, y.x, 0x5410);
                     xw[kp][0][1] = __byte_perm(x.x, y.x, 0x7632);
                     xw[kp][1][0] = __byte_perm(x.y, y.y, 0x5410);
                     xw[kp][1][1] = __byte_perm(x.y, y.y, 0x7632);
                 } else {
                     const uint32_t x = *reinterpret_cast<const uint32_t*>(vc + k0 * VB + 4 * r);
-                    const uint32_t y = *reinterpret_cast<const uint32_t*>(vc + (k0 + 1) * VB + 4 * r);
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(vc + k1 * VB + 4 * r);
                     xw[kp][0][0] = __byte_perm(x, y, 0x5410);
                     xw[kp][0][1] = __byte_perm(x, y, 0x7632);
                 }

@@ -89,9 +89,10 @@ def attention(q, k, v, ksteps, first, scale):
 
     The bound, by term:
       * the weights p_j are rounded to bf16, half a step each (2^-8): 2^-8 sum p |v| / sum p;
-      * a score is off by e_j: the kernel sums (128 + n) q over 32 dims plus -136 sum q, up to 65 terms, each partial
-        sum at most 136 + 143 times sum |q|, each sum off by at most 2^-23 of it (accumulators may truncate), times the
-        step, over all groups; that moves p_j by a factor exp(scale e), in numerator and denominator;
+      * a score is off by e_j: sums of n q over 32 dims plus -8 sum q, up to 65 terms, each partial sum at most 15 + 8
+        times sum |q|, each sum off by at most 2^-23 of it (accumulators may truncate), times the step, over all groups
+        (sums of c step q over 128 dims, partial sums at most 7 step sum |q|, are off by less); that moves p_j by a
+        factor exp(scale e), in numerator and denominator;
       * fp32 sums over the keys: len terms, 2^-23 each, in numerator and denominator; exp2 and the scalings: 2^-20;
       * the result is rounded to bf16: 2^-8 of it."""
     n, heads, D = q.shape
@@ -109,6 +110,6 @@ def attention(q, k, v, ksteps, first, scale):
             out[i] = w @ v[:m]
             spread = w @ np.abs(v[:m])
             per_group = np.abs(q[i]).reshape(heads, -1, GROUP).sum(-1)  # [heads, G]
-            e = scale * 65 * 2.0 ** -23 * 279 * (per_group @ ksteps[:m].astype(np.float64).T).max(-1, keepdims=True)
+            e = scale * 65 * 2.0 ** -23 * 23 * (per_group @ ksteps[:m].astype(np.float64).T).max(-1, keepdims=True)
             bound[i] = spread * (2.0 ** -8 + 2 * np.expm1(e) + 2 * m * 2.0 ** -23 + 2.0 ** -20) + np.abs(out[i]) * 2.0 ** -8
     return out, bound * 1.01 + 1e-30
