@@ -27,6 +27,8 @@
 // of 32 copies ahead loaded at once).
 #include <algorithm>
 
+#include <cfloat>
+
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
 
@@ -466,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                         m = fmaxf(m, mx[nt][e]);
-                        const float now = m == -INFINITY ? 0.0f : m * sc[nt][e];
+                        // a score may lie beyond fp32 where it is taken in binary units: then it weighs nothing, but is no NaN
+                        const float now = m == -INFINITY ? 0.0f : fmaxf(m * sc[nt][e], -FLT_MAX);
                         const float f = exp2_approx(mx[nt][e] == -INFINITY ? -INFINITY : msc[nt][e] - now);
                         mx[nt][e] = m;
                         msc[nt][e] = now;

@@ -27,6 +27,8 @@
 #include <algorithm>
 #include <type_traits>
 
+#include <cfloat>
+
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
 
@@ -138,22 +140,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // 2^x of two values on the multiply-add pipe, for a share of the exponentials
 // (the special-function pipe alone would take as long as the MMAs): x = n + f,
-// |f| <= 1/2, by adding 1.5 * 2^23; 2^f by a cubic (fitted to the least largest
-// relative error, 7.5e-05, a fraction of a bf16 rounding); 2^n as an exponent.
-// x below -127 gives 0, a NaN stays one.
+// |f| <= 1/2, by adding 1.5 * 2^23 + 128; 2^f by a cubic (fitted to the least
+// largest relative error, 7.5e-05, a fraction of a bf16 rounding); 2^n as an
+// exponent. x below -127 gives 0, a NaN stays one. An x of 128 or more gives
+// nonsense: its sum t is no longer POLY_MAGIC plus a byte; `seen`, all sums' bits,
+// shows it (half an instruction a value; a clamp from above, or a maximum of the
+// arguments, made the prompts 3% slower).
+constexpr uint32_t POLY_MAGIC = 0x4B400000u;  // 1.5 * 2^23
 constexpr int POLY_EVERY = 4;
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
+__device__ __forceinline__ float2 exp2_poly(float2 x, uint32_t& seen) {
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
-    const float2 magic = make_float2(12582912.0f, 12582912.0f), minus = make_float2(-12582912.0f, -12582912.0f);
+    const float2 magic = make_float2(12583040.0f, 12583040.0f), minus = make_float2(-12583040.0f, -12583040.0f);
     const float2 t = add2(x, magic);
+    seen |= __float_as_uint(t.x) | __float_as_uint(t.y);
     const float2 n = add2(t, minus);
     const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
     float2 y = fma2(f, make_float2(0.0551713221f, 0.0551713221f), make_float2(0.242610544f, 0.242610544f));
     y = fma2(y, f, make_float2(0.693260968f, 0.693260968f));
     y = fma2(y, f, make_float2(0.999928117f, 0.999928117f));
-    y.x *= __uint_as_float((__float_as_uint(t.x) << 23) + 0x3F800000u);
-    y.y *= __uint_as_float((__float_as_uint(t.y) << 23) + 0x3F800000u);
+    y.x *= __uint_as_float((__float_as_uint(t.x) << 23) - 0x00800000u);
+    y.y *= __uint_as_float((__float_as_uint(t.y) << 23) - 0x00800000u);
     return y;
 }
 
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     }
                 };
                 // Exponentials against the maximum so far. A row whose sum shows that its maximum has grown too much
-                // (always on the first block) has it raised, and the warp takes the pass again: the scores stay where
+                // (always on the first block, and while no score was above -inf) has it raised, and the warp takes the pass again: the scores stay where
                 // they are until P is stored over them. Nothing else looks at the scores' maximum.
                 float sum = 0.0f;
                 uint32_t pk[2][32];
@@ -688,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         }
                         float f = 1.0f;
                         if (m > mx) {
-                            const float now = m * sc;
+                            const float now = fmaxf(m * sc, -FLT_MAX);  // a score beyond fp32 weighs nothing, but is no NaN
                             f = mx == -INFINITY ? 0.0f : exp2_approx(msc - now);
                             mx = m;
                             msc = now;
@@ -706,6 +713,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         }
                     }
                     const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-msc, -msc);
+                    uint32_t top = 0;  // bits of exp2_poly's sums
                     float2 d2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     load(0);
 #pragma unroll
@@ -717,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         for (int x = 0; x < 16; ++x) {
                             float2 e = fma2(make_float2(__uint_as_float(s[k & 1][2 * x]), __uint_as_float(s[k & 1][2 * x + 1])), sc2, off2);
                             if (POLY_EVERY && x % (POLY_EVERY + !POLY_EVERY) == POLY_EVERY - 1) {
-                                e = exp2_poly(e);
+                                e = exp2_poly(e, top);
                             } else {
                                 e.x = exp2_approx(e.x);
                                 e.y = exp2_approx(e.y);
@@ -727,7 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         }
                     }
                     sum = (d2[0].x + d2[0].y) + (d2[1].x + d2[1].y);
-                    if (again || !__any_sync(0xffffffffu, sum > RAISE_SUM)) break;
+                    if (again || !__any_sync(0xffffffffu, sum > RAISE_SUM || (top ^ POLY_MAGIC) > 0xFFu || (mx == -INFINITY && seen > 0))) break;
                     again = true;
                 }
                 tc::tmem_st_32x32(tS, pk[0]);

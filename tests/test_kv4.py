@@ -402,6 +402,41 @@ def test_queries_without_a_softmax(new):
 
 
 @gpu
+@pytest.mark.parametrize("heads", [4, 60])
+def test_a_later_key_may_outweigh_all_before_it_by_any_factor(heads):
+    """One key, at each column of a block in turn, whose weight is 2^gap times that of everything before it."""
+    D, Hk, n = 64, heads // 20 or 1, 512
+    b = Batch([(1, n)] * 128, D, heads, Hk, 64, seed=11)
+    k = np.zeros((128, n, Hk, D), np.float32)
+    v = np.full((128, n, Hk, D), 7.0, np.float32)
+    k[np.arange(128), 256 + np.arange(128)] = 7.0
+    v[np.arange(128), 256 + np.arange(128)] = -3.5
+    b.fill(k.reshape(-1, Hk, D), v.reshape(-1, Hk, D))
+    for gap in (1, 9, 12, 100, 126, 127.4, 128, 150, 260, 390, 500, 1100):
+        q = torch.full((128, heads, D), gap * np.log(2) / (7 * D * D ** -0.5), dtype=torch.bfloat16, device="cuda")
+        out = bl.kv4_attention(q, *b.args(), 1)
+        if gap < 30:
+            b.check(q, out)
+        else:  # the rest weighs less than 512 * 2^-30
+            assert (np_(out.float()) == -3.5).all(), gap
+
+
+@gpu
+@pytest.mark.parametrize("heads", [4, 20])
+def test_scores_that_overflow_downwards_leave_the_rest(heads):
+    """Keys whose score is -inf in fp32 weigh nothing; those behind them do, however low their scores."""
+    D, n = 64, 700
+    b = Batch([(1, n)] * 3, D, heads, 1, 64, seed=12)
+    k = np.full((3, n, 1, D), -3.75e-4, np.float32)
+    v = np.full((3, n, 1, D), 7.0, np.float32)
+    k[:, :300] = -1e35
+    v[:, :300] = -7.0
+    b.fill(k.reshape(-1, 1, D), v.reshape(-1, 1, D))
+    q = torch.full((3, heads, D), 1e5, dtype=torch.bfloat16, device="cuda")
+    assert (np_(bl.kv4_attention(q, *b.args(), 1).float()) == 7.0).all()
+
+
+@gpu
 def test_attention_reads_far_pages_and_shared_ones():
     """Pages whose byte offsets pass 2^31 (and 2^32 in the codes of both arrays), a prefix two sequences share."""
     D, Hk, P = 128, 8, 256
