@@ -3,11 +3,14 @@
 //
 //   y[m, n] = [residual +] fl(fl(float(acc) wstep[n]) fl(1 / s_m))
 //
-// One token (and up to eight with short rows): bound by the N K weight bytes. Warps stream 16 rows at a time
-// from DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A): a
-// lane's 16 bytes of a row are the four words of two MMAs, and the lane's 16 bytes
-// of a token's codes line up with them, so neither side is rearranged. A single
-// token is quantised inside the kernel, by every block for itself.
+// One token: bound by the N K weight bytes. Warps stream 16 rows at a time from
+// DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A): a lane's 16
+// bytes of a row are the four words of two MMAs, and the lane's 16 bytes of the
+// token's codes line up with them, so neither side is rearranged. The token is
+// quantised inside the kernel, by every block for itself: one launch, 4.2 us
+// against 5.5 with a quantiser before the kernel for few tokens (2560 x
+// 2560). 100003 x 2560 with the
+// norm takes 43.6 us, 5.9 TB/s of weights and outputs.
 #include <algorithm>
 
 #include "common.cuh"
@@ -88,25 +91,14 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 }
 
 constexpr int kGemvWarps = 8;
-constexpr int kUnroll = 5;               // 64-byte chunks of a row pair in flight per warp
-constexpr int kGemvTokens = 8;           // most tokens of the GEMV,
-constexpr int kGemvMaxK = 4096;          // and the longest K with more than one (measured: at 6912 the clusters are faster)
-constexpr int kFusedTokens = 1;          // up to here the kernel quantises x itself
-constexpr int kFusedBytes = 32 * 1024;   // and keeps its codes in shared memory (48 KiB with the static part)
-
-struct GemvIn {
-    const uint16_t* x;  // fused: activations to quantise
-    int norm;
-    int pitch;          // fused: bytes from one token's codes to the next
-};
+constexpr int kUnroll = 5;              // 64-byte chunks of a row pair in flight per warp
+constexpr int kGemvMaxK = 32 * 1024;    // its codes stay in shared memory, 48 KiB with the static part
 
 // The kernel's blocks are persistent and take every gridDim.x-th tile of 16 rows; the 8 warps of a block share a
 // tile (64-byte chunks of K in turn), their sums meet in shared memory. The first tile's weights are under way before
 // the kernel waits for the one before it: weights are constants (the header says so for packed weights).
-template <bool FUSED>
-__global__ void __launch_bounds__(32 * kGemvWarps, 4) gemv_int8_kernel(const Int8Args a, const GemvIn in) {
-    __shared__ int part[2][kGemvWarps][4][32];
-    __shared__ float xstep_sh[8];
+__global__ void __launch_bounds__(32 * kGemvWarps, 4) gemv_int8_kernel(const Int8Args a, const uint16_t* x, int norm) {
+    __shared__ int part[2][kGemvWarps][16];
     __shared__ float fscratch[kGemvWarps];
     __shared__ double dscratch[kGemvWarps];
     extern __shared__ __align__(16) int8_t codes[];
@@ -132,82 +124,70 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 4) gemv_int8_kernel(const Int
     grid_dependency_wait();
     grid_dependents_launch();
 
-    if (FUSED) {
-        // as the separate quantiser does it
-        for (int m = 0; m < a.M; ++m) {
-            const uint4* xr = reinterpret_cast<const uint4*>(in.x + (int64_t)m * a.K);
-            float top = 0.0f;
-            double ss = 0.0;
-            for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
-                const uint4 w = xr[c];
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    // the codes, as the separate quantiser makes them
+    const uint4* xr = reinterpret_cast<const uint4*>(x);
+    float top = 0.0f;
+    double ss = 0.0;
+    for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
+        const uint4 w = xr[c];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float lo = __uint_as_float(ws[e] << 16), hi = __uint_as_float(ws[e] & 0xffff0000u);
-                    top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
-                    if (in.norm) ss = __fma_rn((double)lo, (double)lo, __fma_rn((double)hi, (double)hi, ss));
-                }
-            }
-            top = block_max<kGemvWarps>(top, fscratch);
-            float rms = 1.0f;
-            if (in.norm) {
-                ss = block_sum<kGemvWarps>(ss, dscratch);
-                rms = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn((float)(ss / (double)a.K), kRmsEps)));
-                top = __fmul_rn(top, rms);
-            }
-            const float s = __fdiv_rn(kActRange, fmaxf(top, kActEps));
-            if (threadIdx.x == 0) xstep_sh[m] = __fdiv_rn(1.0f, s);
-            for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
-                const uint4 w = xr[c];
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                uint32_t o[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float f = __uint_as_float(e & 1 ? ws[e / 2] & 0xffff0000u : ws[e / 2] << 16);
-                    if (in.norm) f = __fmul_rn(f, rms);
-                    o[e / 4] |= (uint32_t)(quant_code(f, s) & 255) << (8 * (e & 3));
-                }
-                *reinterpret_cast<uint2*>(codes + m * in.pitch + 8 * c) = make_uint2(o[0], o[1]);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(ws[e] << 16), hi = __uint_as_float(ws[e] & 0xffff0000u);
+            top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+            if (norm) ss = __fma_rn((double)lo, (double)lo, __fma_rn((double)hi, (double)hi, ss));
         }
-    } else if (threadIdx.x < a.M) {
-        xstep_sh[threadIdx.x] = __fdiv_rn(1.0f, a.scale[threadIdx.x]);
+    }
+    top = block_max<kGemvWarps>(top, fscratch);
+    float rms = 1.0f;
+    if (norm) {
+        ss = block_sum<kGemvWarps>(ss, dscratch);
+        rms = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn((float)(ss / (double)a.K), kRmsEps)));
+        top = __fmul_rn(top, rms);
+    }
+    const float s = __fdiv_rn(kActRange, fmaxf(top, kActEps)), xstep = __fdiv_rn(1.0f, s);
+    for (int c = threadIdx.x; c < a.K / 8; c += 32 * kGemvWarps) {
+        const uint4 w = xr[c];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float f = __uint_as_float(e & 1 ? ws[e / 2] & 0xffff0000u : ws[e / 2] << 16);
+            if (norm) f = __fmul_rn(f, rms);
+            o[e / 4] |= (uint32_t)(quant_code(f, s) & 255) << (8 * (e & 3));
+        }
+        *reinterpret_cast<uint2*>(codes + 8 * c) = make_uint2(o[0], o[1]);
     }
     __syncthreads();
 
-    const bool live = r < a.M;
-    const int8_t* x = (FUSED ? codes + min(r, a.M - 1) * in.pitch : a.xq + (int64_t)min(r, a.M - 1) * a.K) + 16 * t;
     int turn = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
-        // the output this thread stores after the sums have met: accumulator element `warp` of its lane
-        const int n = tile * 16 + r + 8 * ((warp & 3) >> 1);
-        const float ws = warp < 4 && n < a.N ? a.wstep[n] : 0.0f;
-        int d[4] = {0, 0, 0, 0};
+        const int n = tile * 16 + (int)threadIdx.x;  // the row this thread finishes, if it is one of the first 16
+        const bool last = threadIdx.x < 16 && n < a.N;
+        const float ws = last ? a.wstep[n] : 0.0f;
+        int d[4] = {0, 0, 0, 0};  // the token is column 0: d[0] and d[2] of lanes with t = 0
         for (int c = warp; c < n_chunks; c += kGemvWarps * kUnroll) {
             if (c != warp || tile != blockIdx.x) load(tile, c);
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
-                const int k = (c + i * kGemvWarps) * 64;
-                const uint4 b = k + 16 * t < a.K && live ? *reinterpret_cast<const uint4*>(x + k) : zero;
+                const int k = (c + i * kGemvWarps) * 64 + 16 * t;
+                const uint4 b = k < a.K && r == 0 ? *reinterpret_cast<const uint4*>(codes + k) : zero;
                 mma_s8(d, u[i].x, v[i].x, u[i].y, v[i].y, b.x, b.y);
                 mma_s8(d, u[i].z, v[i].z, u[i].w, v[i].w, b.z, b.w);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[turn][warp][e][lane] = d[e];
+        if (t == 0) part[turn][warp][r] = d[0], part[turn][warp][r + 8] = d[2];
         __syncthreads();  // the other half of `part` is free: every warp has passed the tile before
-        if (warp < 4) {
+        if (last) {
             int acc = 0;
 #pragma unroll
-            for (int w = 0; w < kGemvWarps; ++w) acc += part[turn][w][warp][lane];
-            const int m = 2 * t + (warp & 1);
-            if (n < a.N && m < a.M) store_one(a, m, n, acc, ws, xstep_sh[m]);
+            for (int w = 0; w < kGemvWarps; ++w) acc += part[turn][w][threadIdx.x];
+            store_one(a, 0, n, acc, ws, xstep);
         }
     }
 }
 
-template <bool FUSED>
-cudaError_t launch_gemv(const Int8Args& a, const GemvIn& in, cudaStream_t s) {
+cudaError_t launch_gemv(const Int8Args& a, const uint16_t* x, bool norm, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -215,18 +195,16 @@ cudaError_t launch_gemv(const Int8Args& a, const GemvIn& in, cudaStream_t s) {
     if (dev >= 64 || !resident[dev]) {
         int sms = 0, per = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, gemv_int8_kernel<FUSED>, 32 * kGemvWarps, FUSED ? 8192 : 0);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, gemv_int8_kernel, 32 * kGemvWarps, 8192);
         if (e != cudaSuccess) return e;
         if (dev < 64) resident[dev] = sms * per;
     }
     const int tiles = (a.N + 15) / 16;
     const int grid = std::min(tiles, dev < 64 ? resident[dev] : 148);
-    return launch_pdl(gemv_int8_kernel<FUSED>, dim3((unsigned)grid), dim3(32 * kGemvWarps),
-                      FUSED ? (size_t)in.pitch * a.M : 0, s, a, in);
+    return launch_pdl(gemv_int8_kernel, dim3((unsigned)grid), dim3(32 * kGemvWarps), (size_t)a.K, s, a, x, norm ? 1 : 0);
 }
 
-// ---------------------------------------------------------------- M > 16: tcgen05
+// ---------------------------------------------------------------- M > 128: tcgen05
 //
 // M > 128: TMA brings 128 bytes of K of 128 tokens and BN weight rows per stage, one thread issues tcgen05.mma kind::i8
 // into one of two int32 accumulators in TMEM, four warps read the other one out. Persistent blocks take whole tiles;
@@ -431,10 +409,65 @@ struct FewArgs {
     int stages, cols, log_split;  // ring stages, tokens rounded up to 16, log2 of the blocks per tile
 };
 
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+
+// A block's share of its tile's rows, of 2^LS blocks' sums [token][128 rows] in shared memory: a thread keeps four
+// neighbouring rows.
+template <int LS>
+__device__ __forceinline__ void finish_rows(const Int8Args& a, const int* sums, const float* xstep, int n0, int rank, int et) {
+    constexpr int ROWS = BM >> LS, QUADS = ROWS / 4;
+    const int row = rank * ROWS + et % QUADS * 4, n = n0 + row;
+    if (n >= a.N) return;
+    const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y16) | reinterpret_cast<uintptr_t>(a.y32) |
+                                      reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.acc)) % 16 == 0;
+    float ws[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ws[e] = n + e < a.N ? a.wstep[n + e] : 0.0f;
+    uint32_t at[1 << LS];
+#pragma unroll
+    for (int p = 0; p < 1 << LS; ++p) at[p] = LS ? tc::map_to_rank(tc::smem_u32(sums + row), p) : 0;
+#pragma unroll 1
+    for (int m = et / QUADS; m < a.M; m += 32 * EPI_WARPS / QUADS) {
+        int v[4];
+        if constexpr (LS == 0) {
+            const int4 x = *reinterpret_cast<const int4*>(sums + m * BM + row);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            int4 x[1 << LS];
+#pragma unroll
+            for (int p = 0; p < 1 << LS; ++p) x[p] = ld_cluster(at[p] + m * BM * 4);
+            v[0] = v[1] = v[2] = v[3] = 0;
+#pragma unroll
+            for (int p = 0; p < 1 << LS; ++p) v[0] += x[p].x, v[1] += x[p].y, v[2] += x[p].z, v[3] += x[p].w;
+        }
+        if (!vec) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < a.N) store_one(a, m, n + e, v[e], ws[e], xstep[m]);
+            continue;
+        }
+        const int64_t o = (int64_t)m * a.N + n;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __fmul_rn(__fmul_rn((float)v[e], ws[e]), xstep[m]);
+        if (a.residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(a.residual + o);
+            y[0] = __fadd_rn(bf16_bits_to_f32(r.x & 0xffffu), y[0]);
+            y[1] = __fadd_rn(bf16_bits_to_f32(r.x >> 16), y[1]);
+            y[2] = __fadd_rn(bf16_bits_to_f32(r.y & 0xffffu), y[2]);
+            y[3] = __fadd_rn(bf16_bits_to_f32(r.y >> 16), y[3]);
+        }
+        if (a.y32)
+            *reinterpret_cast<float4*>(a.y32 + o) = make_float4(y[0], y[1], y[2], y[3]);
+        else
+            *reinterpret_cast<uint2*>(a.y16 + o) = make_uint2(f32_to_bf16_bits(y[0]) | (uint32_t)f32_to_bf16_bits(y[1]) << 16,
+                                                              f32_to_bf16_bits(y[2]) | (uint32_t)f32_to_bf16_bits(y[3]) << 16);
+        if (a.acc) *reinterpret_cast<int4*>(a.acc + o) = make_int4(v[0], v[1], v[2], v[3]);
+    }
 }
 
 __global__ void __launch_bounds__(GEMM_THREADS)
@@ -547,20 +580,12 @@ __global__ void __launch_bounds__(GEMM_THREADS)
     else
         __syncthreads();
     if (warp >= 2 && !*aborted) {
-        // this block finishes rows rank * rows .. of the tile; a thread keeps its row
-        const int rows = BM >> f.log_split, et = threadIdx.x - 64;
-        const int row = rank * rows + (et & (rows - 1)), n = n0 + row;
-        if (n < a.N) {
-            const float ws = a.wstep[n];
-            for (int m = et / rows; m < a.M; m += 1 << f.log_split) {
-                int acc = sums[m * BM + row];
-                if (f.log_split) {
-                    const uint32_t at = tc::smem_u32(sums + m * BM + row);
-                    acc = 0;
-                    for (int p = 0; p < 1 << f.log_split; ++p) acc += ld_cluster(tc::map_to_rank(at, p));
-                }
-                store_one(a, m, n, acc, ws, xstep_sh[m]);
-            }
+        const int et = threadIdx.x - 64;
+        switch (f.log_split) {
+            case 0: finish_rows<0>(a, sums, xstep_sh, n0, rank, et); break;
+            case 1: finish_rows<1>(a, sums, xstep_sh, n0, rank, et); break;
+            case 2: finish_rows<2>(a, sums, xstep_sh, n0, rank, et); break;
+            default: finish_rows<3>(a, sums, xstep_sh, n0, rank, et);
         }
     }
     if (f.log_split)
@@ -576,8 +601,14 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
     f.cols = (a.M + 15) / 16 * 16;
     f.stages = std::min(FEW_STAGES_MAX, (FEW_SMEM - 1024) / (A_BYTES + f.cols * BK));
     const int tiles = (a.N + BM - 1) / BM, nkb = (a.K + BK - 1) / BK;
-    f.log_split = 0;  // up to two blocks per SM and 8 per cluster, at least two k-blocks each
-    while (f.log_split < 3 && (tiles << (f.log_split + 1)) <= 2 * sms && nkb >= 4 << f.log_split) ++f.log_split;
+    // Up to 8 blocks per tile with at least two k-blocks each, one block per SM. Two blocks per SM save half a block's
+    // loads and make the meeting of the sums dearer, the more tokens the more: with 4 k-blocks left each (K = 4096)
+    // 8.4 against 8.7 us for 16 tokens, but 13.6 against 11.7 for 128; with 6.75 (K = 6912) 14.6 against 15.2 for 128.
+    f.log_split = 0;
+    for (; f.log_split < 3; ++f.log_split) {
+        const int blocks = tiles << (f.log_split + 1), least = blocks <= sms ? 2 : std::min(2 + f.cols / 16, 6);
+        if (blocks > 2 * sms || nkb < least << (f.log_split + 1)) break;
+    }
     CUtensorMap mapW, mapX;
     if (!make_map(&mapW, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BM, BK, true) ||
         !make_map(&mapX, a.xq, (uint64_t)a.M, (uint64_t)a.K, (uint32_t)f.cols, BK, true))
@@ -657,11 +688,9 @@ cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t
                         int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
                         cudaStream_t s) {
     Int8Args a{Wq, wstep, xq, scale, residual, y16, y32, acc, (int)M, (int)N, (int)K};
-    const GemvIn in{x, rmsnorm ? 1 : 0, (int)K + 16};
-    if (M <= kFusedTokens && M * in.pitch <= kFusedBytes) return launch_gemv<true>(a, in, s);
+    if (M == 1 && K <= kGemvMaxK) return launch_gemv(a, x, rmsnorm, s);
     cudaError_t e = launch_act_quant(x, M, K, XQ_NATURAL, xq, scale, nullptr, s, rmsnorm);
     if (e != cudaSuccess) return e;
-    if (M <= kGemvTokens && K <= kGemvMaxK) return launch_gemv<false>(a, in, s);
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
