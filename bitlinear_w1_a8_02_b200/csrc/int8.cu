@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 // tile each. Their int32 sums meet through distributed shared memory: each block finishes its share of the rows.
 // Weight loads start before the kernel waits for the one before it.
 constexpr int FEW_MAX = 128;
-constexpr int FEW_SMEM = 104 * 1024;  // two blocks per SM
+constexpr int FEW_SMEM[3] = {55 * 1024, 74 * 1024, 104 * 1024};  // four, three, two blocks per SM
 constexpr int FEW_STAGES_MAX = 6;
 
 struct FewArgs {
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(GEMM_THREADS)
 cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
     FewArgs f;
     f.cols = (a.M + 15) / 16 * 16;
-    f.stages = std::min(FEW_STAGES_MAX, (FEW_SMEM - 1024) / (A_BYTES + f.cols * BK));
+    const int stage = A_BYTES + f.cols * BK;
     const int tiles = (a.N + BM - 1) / BM, nkb = (a.K + BK - 1) / BK;
     // Up to 8 blocks per tile with at least two k-blocks each, one block per SM. Two blocks per SM save half a block's
     // loads and make the meeting of the sums dearer, the more tokens the more: with 4 k-blocks left each (K = 4096)
@@ -609,6 +609,10 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
         const int blocks = tiles << (f.log_split + 1), least = blocks <= sms ? 2 : std::min(2 + f.cols / 16, 6);
         if (blocks > 2 * sms || nkb < least << (f.log_split + 1)) break;
     }
+    // Deep rings where every block is resident; else as many blocks per SM as keep two stages (the sums need two), so
+    // that some load while others start or finish.
+    const int room = tiles <= 2 * sms ? 2 : 2 * stage + 1024 <= FEW_SMEM[0] ? 0 : 1;
+    f.stages = std::min(FEW_STAGES_MAX, (FEW_SMEM[room] - 1024) / stage);
     CUtensorMap mapW, mapX;
     if (!make_map(&mapW, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BM, BK, true) ||
         !make_map(&mapX, a.xq, (uint64_t)a.M, (uint64_t)a.K, (uint32_t)f.cols, BK, true))
@@ -618,14 +622,14 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     static bool attr_set[64];
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(few_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
+        e = cudaFuncSetAttribute(few_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM[2]);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles << f.log_split));
     cfg.blockDim = dim3(GEMM_THREADS);
-    cfg.dynamicSmemBytes = (size_t)1024 + f.stages * (A_BYTES + f.cols * BK);
+    cfg.dynamicSmemBytes = (size_t)1024 + f.stages * stage;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
