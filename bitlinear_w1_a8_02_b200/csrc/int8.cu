@@ -93,6 +93,10 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 constexpr int kGemvWarps = 8;
 constexpr int kUnroll = 5;              // 64-byte chunks of a row pair in flight per warp
 constexpr int kGemvMaxK = 32 * 1024;    // its codes stay in shared memory, 48 KiB with the static part
+// Many short rows go to the kernel for few tokens instead, whose tiles of 128 rows meet less often (one token, here
+// against there): 4096 x 256 2.7 and 4.1 us, 16384 x 768 6.5 and 7.1, 32768 x 2048 14.8 and 15.7; 16384 x 256 4.4 and
+// 4.2, 32768 x 1024 10.8 and 10.0, 80000 x 768 18.7 and 14.9, 128256 x 2560 53.3 and 52.0.
+constexpr int64_t kGemvRows = 8192, kGemvRatio = 24;
 
 // The kernel's blocks are persistent and take every gridDim.x-th tile of 16 rows; the 8 warps of a block share a
 // tile (64-byte chunks of K in turn), their sums meet in shared memory. The first tile's weights are under way before
@@ -692,7 +696,7 @@ cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t
                         int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
                         cudaStream_t s) {
     Int8Args a{Wq, wstep, xq, scale, residual, y16, y32, acc, (int)M, (int)N, (int)K};
-    if (M == 1 && K <= kGemvMaxK) return launch_gemv(a, x, rmsnorm, s);
+    if (M == 1 && K <= kGemvMaxK && (N <= kGemvRows || N <= kGemvRatio * K)) return launch_gemv(a, x, rmsnorm, s);
     cudaError_t e = launch_act_quant(x, M, K, XQ_NATURAL, xq, scale, nullptr, s, rmsnorm);
     if (e != cudaSuccess) return e;
     int dev = 0;
