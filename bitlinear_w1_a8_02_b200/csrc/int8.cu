@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
+    __shared__ int turn_sh[EPI_WARPS][32][33];
     uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sB = sA + STAGES * A_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sB + STAGES * B_BYTES);
@@ -340,45 +341,57 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 tc::tmem_ld_32x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + b * BN + c * 32, v);
                 tc::tmem_ld_wait();
                 const int nb = n0 + c * 32;
-                if (!mv || nb >= a.N) continue;
+                if (nb >= a.N) break;
+                if (!vec || nb + 32 > a.N) {
+                    // rows without 16-byte alignment: through shared memory, so that a lane has a column and a warp
+                    // stores 32 neighbouring values of a row
+                    int(&turn)[32][33] = turn_sh[q];
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) turn[lane][j] = (int)v[j];
+                    __syncwarp();
+                    const int n = nb + lane, rows = min(32, a.M - (m - lane));
+                    const float ws = n < a.N ? a.wstep[n] : 0.0f;
+#pragma unroll 8
+                    for (int row = 0; row < rows; ++row) {
+                        const float xs = __shfl_sync(0xffffffffu, xstep, row);
+                        if (n < a.N) store_one(a, m - lane + row, n, turn[row][lane], ws, xs);
+                    }
+                    continue;
+                }
+                if (!mv) continue;
                 const int64_t o = (int64_t)m * a.N + nb;
-                if (vec && nb + 32 <= a.N) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        float f[8];
-                        const float4 wa = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j));
-                        const float4 wb = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j + 4));
-                        const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                for (int j = 0; j < 32; j += 8) {
+                    float f[8];
+                    const float4 wa = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j));
+                    const float4 wb = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j + 4));
+                    const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn((float)(int)v[j + e], ws[e]), xstep);
-                        if (a.residual) {
-                            const uint4 rr = *reinterpret_cast<const uint4*>(a.residual + o + j);
-                            const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
+                    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn((float)(int)v[j + e], ws[e]), xstep);
+                    if (a.residual) {
+                        const uint4 rr = *reinterpret_cast<const uint4*>(a.residual + o + j);
+                        const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                f[2 * e] = __fadd_rn(bf16_bits_to_f32(rw[e] & 0xffffu), f[2 * e]);
-                                f[2 * e + 1] = __fadd_rn(bf16_bits_to_f32(rw[e] >> 16), f[2 * e + 1]);
-                            }
-                        }
-                        if (a.y32) {
-                            *reinterpret_cast<float4*>(a.y32 + o + j) = make_float4(f[0], f[1], f[2], f[3]);
-                            *reinterpret_cast<float4*>(a.y32 + o + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
-                        } else {
-                            uint32_t pk[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                pk[e] = f32_to_bf16_bits(f[2 * e]) | (uint32_t)f32_to_bf16_bits(f[2 * e + 1]) << 16;
-                            *reinterpret_cast<uint4*>(a.y16 + o + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        }
-                        if (a.acc) {
-                            *reinterpret_cast<int4*>(a.acc + o + j) = make_int4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                            *reinterpret_cast<int4*>(a.acc + o + j + 4) = make_int4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                        for (int e = 0; e < 4; ++e) {
+                            f[2 * e] = __fadd_rn(bf16_bits_to_f32(rw[e] & 0xffffu), f[2 * e]);
+                            f[2 * e + 1] = __fadd_rn(bf16_bits_to_f32(rw[e] >> 16), f[2 * e + 1]);
                         }
                     }
-                } else {
+                    if (a.y32) {
+                        *reinterpret_cast<float4*>(a.y32 + o + j) = make_float4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<float4*>(a.y32 + o + j + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                    } else {
+                        uint32_t pk[4];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (nb + j < a.N) store_one(a, m, nb + j, (int)v[j], a.wstep[nb + j], xstep);
+                        for (int e = 0; e < 4; ++e)
+                            pk[e] = f32_to_bf16_bits(f[2 * e]) | (uint32_t)f32_to_bf16_bits(f[2 * e + 1]) << 16;
+                        *reinterpret_cast<uint4*>(a.y16 + o + j) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    if (a.acc) {
+                        *reinterpret_cast<int4*>(a.acc + o + j) = make_int4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        *reinterpret_cast<int4*>(a.acc + o + j + 4) = make_int4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                    }
                 }
             }
             tc::fence_before_sync();

@@ -15,7 +15,10 @@ namespace bl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kFewTokens = 512;  // below: one step a warp
+// Below: one step a warp, so that the look-ups overlap. Append of 64 tokens 2.7 us against 3.8 with five steps, 256
+// tokens 4.4 and 5.0; 384 tokens 6.1 and 5.9, 2048 of one sequence 12.4 and 8.8. Read: 2.1 and 2.3, 3.4 and 3.6, 4.3 and
+// 4.4, 3.3 and 2.8 (20 query and 5 key/value heads of 128).
+constexpr int64_t kFewTokens = 384;
 
 struct AppendArgs {
     const uint16_t *q, *k, *v;
