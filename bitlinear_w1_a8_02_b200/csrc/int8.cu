@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     __shared__ int turn_sh[EPI_WARPS][32][33];
+    __shared__ __align__(16) float ws_sh[EPI_WARPS][BN];  // a warp's copy of the tile's weight steps
     uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sB = sA + STAGES * A_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sB + STAGES * B_BYTES);
@@ -321,20 +322,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     } else {
         const int q = warp & 3;  // the TMEM lane quarter this warp may read
         const bool vec = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y16) | reinterpret_cast<uintptr_t>(a.y32) |
-                                          reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.acc) |
-                                          reinterpret_cast<uintptr_t>(a.wstep)) % 16 == 0;
+                                          reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.acc)) % 16 == 0;
         uint32_t t = 0;
         for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++t) {
             const int b = t & 1;
+            const int m = (tile % m_tiles) * BM + q * 32 + lane, n0 = (tile / m_tiles) * BN;
+            const bool mv = m < a.M;
+            const float xstep = mv ? __fdiv_rn(1.0f, a.scale[m]) : 0.0f;
+            __syncwarp();
+            for (int c = lane; c < BN; c += 32) ws_sh[q][c] = n0 + c < a.N ? a.wstep[n0 + c] : 0.0f;
+            __syncwarp();
             const bool ok = !*aborted && tc::mbar_wait(afull(b), (t >> 1) & 1, WAIT_LIMIT_NS);
             if (!__all_sync(0xffffffffu, ok)) {  // tcgen05.ld below is warp-collective
                 give_up();
                 break;
             }
             tc::fence_after_sync();
-            const int m = (tile % m_tiles) * BM + q * 32 + lane, n0 = (tile / m_tiles) * BN;
-            const bool mv = m < a.M;
-            const float xstep = mv ? __fdiv_rn(1.0f, a.scale[m]) : 0.0f;
 #pragma unroll 1
             for (int c = 0; c < BN / 32; ++c) {
                 uint32_t v[32];
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     for (int j = 0; j < 32; ++j) turn[lane][j] = (int)v[j];
                     __syncwarp();
                     const int n = nb + lane, rows = min(32, a.M - (m - lane));
-                    const float ws = n < a.N ? a.wstep[n] : 0.0f;
+                    const float ws = ws_sh[q][c * 32 + lane];
 #pragma unroll 8
                     for (int row = 0; row < rows; ++row) {
                         const float xs = __shfl_sync(0xffffffffu, xstep, row);
@@ -364,8 +367,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
                     float f[8];
-                    const float4 wa = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j));
-                    const float4 wb = __ldg(reinterpret_cast<const float4*>(a.wstep + nb + j + 4));
+                    const float4 wa = *reinterpret_cast<const float4*>(&ws_sh[q][c * 32 + j]);
+                    const float4 wb = *reinterpret_cast<const float4*>(&ws_sh[q][c * 32 + j + 4]);
                     const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn((float)(int)v[j + e], ws[e]), xstep);
