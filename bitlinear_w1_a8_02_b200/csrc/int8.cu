@@ -71,15 +71,18 @@ struct Int8Args {
     int M, N, K;
 };
 
-__device__ __forceinline__ void store_one(const Int8Args& a, int m, int n, int acc, float wstep, float xstep) {
-    const int64_t i = (int64_t)m * a.N + n;
-    float f = __fmul_rn(__fmul_rn((float)acc, wstep), xstep);
+// Output i of the sum acc, whose scaled value is f.
+__device__ __forceinline__ void put_one(const Int8Args& a, int64_t i, int acc, float f) {
     if (a.residual) f = __fadd_rn(bf16_bits_to_f32(a.residual[i]), f);
     if (a.y32)
         a.y32[i] = f;
     else
         a.y16[i] = f32_to_bf16_bits(f);
     if (a.acc) a.acc[i] = acc;
+}
+
+__device__ __forceinline__ void store_one(const Int8Args& a, int m, int n, int acc, float wstep, float xstep) {
+    put_one(a, (int64_t)m * a.N + n, acc, __fmul_rn(__fmul_rn((float)acc, wstep), xstep));
 }
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -211,11 +214,11 @@ cudaError_t launch_gemv(const Int8Args& a, const uint16_t* x, bool norm, cudaStr
 // ---------------------------------------------------------------- M > 128: tcgen05
 //
 // M > 128: TMA brings 128 bytes of K of 128 tokens and BN weight rows per stage, one thread issues tcgen05.mma kind::i8
-// into one of two int32 accumulators in TMEM, four warps read the other one out. Persistent blocks take whole tiles;
+// into one of two int32 accumulators in TMEM, eight warps read the other one out. Persistent blocks take whole tiles;
 // weight tiles are shared by consecutive tiles.
 constexpr int BM = 128, BK = 128;
 constexpr int A_BYTES = BM * BK;
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = 8;  // two to a quarter of TMEM's lanes, 32 columns in turn
 constexpr int GEMM_THREADS = 64 + 32 * EPI_WARPS;
 template <int BN>
 struct Gemm {
@@ -223,6 +226,7 @@ struct Gemm {
     static constexpr int STAGES = BN == 256 ? 4 : 6;
     static constexpr int BARS = 2 * STAGES + 4;
     static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + BARS * 8;
+    static_assert(SMEM + EPI_WARPS * 4 * (16 * 33 + BN) + 16 <= 227 * 1024, "shared memory of a block");
 };
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
-    __shared__ int turn_sh[EPI_WARPS][32][33];
+    __shared__ int turn_sh[EPI_WARPS][16][33];
     __shared__ __align__(16) float ws_sh[EPI_WARPS][BN];  // a warp's copy of the tile's weight steps
     uint8_t* sA = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sB = sA + STAGES * A_BYTES;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const bool mv = m < a.M;
             const float xstep = mv ? __fdiv_rn(1.0f, a.scale[m]) : 0.0f;
             __syncwarp();
-            for (int c = lane; c < BN; c += 32) ws_sh[q][c] = n0 + c < a.N ? a.wstep[n0 + c] : 0.0f;
+            for (int c = lane; c < BN; c += 32) ws_sh[warp - 2][c] = n0 + c < a.N ? a.wstep[n0 + c] : 0.0f;
             __syncwarp();
             const bool ok = !*aborted && tc::mbar_wait(afull(b), (t >> 1) & 1, WAIT_LIMIT_NS);
             if (!__all_sync(0xffffffffu, ok)) {  // tcgen05.ld below is warp-collective
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
             tc::fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = (warp - 2) / 4; c < BN / 32; c += EPI_WARPS / 4) {
                 uint32_t v[32];
                 tc::tmem_ld_32x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + b * BN + c * 32, v);
                 tc::tmem_ld_wait();
@@ -348,17 +352,37 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                 if (!vec || nb + 32 > a.N) {
                     // rows without 16-byte alignment: through shared memory, so that a lane has a column and a warp
                     // stores 32 neighbouring values of a row
-                    int(&turn)[32][33] = turn_sh[q];
-                    __syncwarp();
+                    int(&turn)[16][33] = turn_sh[warp - 2];
+                    const int n = nb + lane, m0 = m - lane, rows = min(32, a.M - m0);
+                    const float ws = ws_sh[warp - 2][c * 32 + lane];
+                    const int64_t o = (int64_t)m0 * a.N + n;
+                    const bool plain = a.y16 && !a.residual && !a.acc;
+                    for (int r0 = 0; r0 < rows; r0 += 8) {
+                        if (r0 % 16 == 0) {
+                            __syncwarp();
+                            if (lane / 16 == r0 / 16) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) turn[lane][j] = (int)v[j];
-                    __syncwarp();
-                    const int n = nb + lane, rows = min(32, a.M - (m - lane));
-                    const float ws = ws_sh[q][c * 32 + lane];
-#pragma unroll 8
-                    for (int row = 0; row < rows; ++row) {
-                        const float xs = __shfl_sync(0xffffffffu, xstep, row);
-                        if (n < a.N) store_one(a, m - lane + row, n, turn[row][lane], ws, xs);
+                                for (int j = 0; j < 32; ++j) turn[lane & 15][j] = (int)v[j];
+                            }
+                            __syncwarp();
+                        }
+                        int acc[8];
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            acc[e] = turn[(r0 & 15) + e][lane];
+                            f[e] = __fmul_rn(__fmul_rn((float)acc[e], ws), __shfl_sync(0xffffffffu, xstep, r0 + e));
+                        }
+                        if (n >= a.N) continue;
+                        if (plain) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (r0 + e < rows) a.y16[o + (int64_t)(r0 + e) * a.N] = f32_to_bf16_bits(f[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (r0 + e < rows) put_one(a, o + (int64_t)(r0 + e) * a.N, acc[e], f[e]);
+                        }
                     }
                     continue;
                 }
@@ -367,8 +391,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
                     float f[8];
-                    const float4 wa = *reinterpret_cast<const float4*>(&ws_sh[q][c * 32 + j]);
-                    const float4 wb = *reinterpret_cast<const float4*>(&ws_sh[q][c * 32 + j + 4]);
+                    const float4 wa = *reinterpret_cast<const float4*>(&ws_sh[warp - 2][c * 32 + j]);
+                    const float4 wb = *reinterpret_cast<const float4*>(&ws_sh[warp - 2][c * 32 + j + 4]);
                     const float ws[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn((float)(int)v[j + e], ws[e]), xstep);
@@ -422,6 +446,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 // tile each. Their int32 sums meet through distributed shared memory: each block finishes its share of the rows.
 // Weight loads start before the kernel waits for the one before it.
 constexpr int FEW_MAX = 128;
+constexpr int FEW_EPI = 128, FEW_THREADS = 64 + FEW_EPI;
 constexpr int FEW_SMEM[3] = {55 * 1024, 74 * 1024, 104 * 1024};  // four, three, two blocks per SM
 constexpr int FEW_STAGES_MAX = 6;
 
@@ -451,7 +476,7 @@ __device__ __forceinline__ void finish_rows(const Int8Args& a, const int* sums, 
 #pragma unroll
     for (int p = 0; p < 1 << LS; ++p) at[p] = LS ? tc::map_to_rank(tc::smem_u32(sums + row), p) : 0;
 #pragma unroll 1
-    for (int m = et / QUADS; m < a.M; m += 32 * EPI_WARPS / QUADS) {
+    for (int m = et / QUADS; m < a.M; m += FEW_EPI / QUADS) {
         int v[4];
         if constexpr (LS == 0) {
             const int4 x = *reinterpret_cast<const int4*>(sums + m * BM + row);
@@ -490,7 +515,7 @@ __device__ __forceinline__ void finish_rows(const Int8Args& a, const int* sums, 
     }
 }
 
-__global__ void __launch_bounds__(GEMM_THREADS)
+__global__ void __launch_bounds__(FEW_THREADS)
     few_int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Args a,
                     const FewArgs f, unsigned* err) {
     extern __shared__ uint8_t smem_raw[];
@@ -648,7 +673,7 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles << f.log_split));
-    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = (size_t)1024 + f.stages * stage;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
