@@ -449,93 +449,88 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     tc::mbar_wait(cfull(h % CODE_STAGES), (h / CODE_STAGES) & 1, WAIT_NS);
             }
         } else if (warp == MMA_WARP) {
-            // ------------------------------------------------------------ MMA issuer (the whole warp walks along;
-            // one elected lane issues)
-            constexpr uint32_t id_s = idesc_bf16(TM, BLK, false);
-            constexpr uint32_t id_o = idesc_bf16(TM, D, true);
-            Pieces p = start_sh;
-            uint32_t n = 0;                // blocks so far (K tile 2n, V tile 2n + 1 of the ring)
-            uint32_t np0 = 0, np1 = 0;     // P tiles consumed
-            uint32_t nq0 = 0, nq1 = 0;     // Q tiles consumed
-            const uint32_t q_lo = desc_lo(tc::smem_u32(sQ), 16);
-            const uint32_t k_lo = desc_lo(tc::smem_u32(sT), 16), v_lo = desc_lo(tc::smem_u32(sT), C::HALF);
-            const bool leader = elect_one();
-            int b0, b1;
-            bool ok = true;
-            auto wait = [&](uint32_t b, uint32_t parity) {
-                ok = tc::mbar_wait(b, parity, WAIT_NS);
-                tc::fence_after_sync();
-                return ok;
-            };
-            auto commit = [&](uint32_t b) {
-                if (leader) tc::mma_commit(b);
-            };
-            // `st` 0 / 1: the half of the ring (K tile 2 st, V tile 2 st + 1), a constant so that descriptors are too
-            auto scores = [&](auto tile, auto st) {
-                constexpr int i = decltype(tile)::value, o = 2 * decltype(st)::value * (C::TILE >> 4);
-                if (leader) {
+            // ------------------------------------------------------------ MMA issuer: one elected lane. (A warp that
+            // walks along is 2% slower and must vote after every wait: a lane that falls behind misses a phase.)
+            if (elect_one()) {
+                constexpr uint32_t id_s = idesc_bf16(TM, BLK, false);
+                constexpr uint32_t id_o = idesc_bf16(TM, D, true);
+                Pieces p = start_sh;
+                uint32_t n = 0;                // blocks so far (K tile 2n, V tile 2n + 1 of the ring)
+                uint32_t np0 = 0, np1 = 0;     // P tiles consumed
+                uint32_t nq0 = 0, nq1 = 0;     // Q tiles consumed
+                const uint32_t q_lo = desc_lo(tc::smem_u32(sQ), 16);
+                const uint32_t k_lo = desc_lo(tc::smem_u32(sT), 16), v_lo = desc_lo(tc::smem_u32(sT), C::HALF);
+                int b0, b1;
+                bool ok = true;
+                auto wait = [&](uint32_t b, uint32_t parity) {
+                    ok = tc::mbar_wait(b, parity, WAIT_NS);
+                    tc::fence_after_sync();
+                    return ok;
+                };
+                auto commit = [&](uint32_t b) { tc::mma_commit(b); };
+                // `st` 0 / 1: the half of the ring (K tile 2 st, V tile 2 st + 1), a constant so that descriptors are too
+                auto scores = [&](auto tile, auto st) {
+                    constexpr int i = decltype(tile)::value, o = 2 * decltype(st)::value * (C::TILE >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * C::HALF + (k % 4) * 32) >> 4;
                         mma_ss(tmem + 128 * i, q_lo + i * (C::TILE >> 4) + off, k_lo + o + off, id_s, k != 0);
                     }
                     tc::mma_commit(sfull(i));
-                }
-            };
-            auto values = [&](auto tile, auto st, bool first) {
-                constexpr int i = decltype(tile)::value, o = (2 * decltype(st)::value + 1) * (C::TILE >> 4);
-                if (leader) {
+                };
+                auto values = [&](auto tile, auto st, bool first) {
+                    constexpr int i = decltype(tile)::value, o = (2 * decltype(st)::value + 1) * (C::TILE >> 4);
 #pragma unroll
                     for (int k = 0; k < BLK / 16; ++k)
                         mma_ts(tmem + 256 + i * D, tmem + 128 * i + 8 * k, v_lo + o + ((k * 16 * 128) >> 4), id_o, k != 0 || !first);
+                };
+                using T0 = std::integral_constant<int, 0>;
+                using T1 = std::integral_constant<int, 1>;
+                // scores of an item's first block (block n of this CTA, in half `st` of the ring)
+                auto open = [&](auto st, bool two) {
+                    constexpr int h = decltype(st)::value;
+                    if (!wait(tfull(2 * h), (n >> 1) & 1) || !wait(qfull(0), nq0++ & 1)) return false;
+                    scores(T0{}, st);
+                    if (two) {
+                        if (!wait(qfull(1), nq1++ & 1)) return false;
+                        scores(T1{}, st);
+                    }
+                    commit(tempty(2 * h));
+                    return true;
+                };
+                // values of block n, scores of block n + 1 if the piece has it: tile 0, then tile 1
+                auto step = [&](auto st, bool two, bool first, bool more) {
+                    constexpr int h = decltype(st)::value;
+                    using Next = std::integral_constant<int, 1 - h>;
+                    if (!wait(tfull(2 * h + 1), (n >> 1) & 1)) return false;
+                    if (more && !wait(tfull(2 * (1 - h)), ((n + 1) >> 1) & 1)) return false;
+                    if (!wait(pfull(0), np0++ & 1)) return false;
+                    values(T0{}, st, first);
+                    if (more)
+                        scores(T0{}, Next{});
+                    else
+                        commit(ofull(0));
+                    if (two) {
+                        if (!wait(pfull(1), np1++ & 1)) return false;
+                        values(T1{}, st, first);
+                        if (!more) commit(ofull(1));
+                    }
+                    commit(tempty(2 * h + 1));
+                    if (more) {
+                        if (two) scores(T1{}, Next{});
+                        commit(tempty(2 * (1 - h)));
+                    }
+                    ++n;
+                    return true;
+                };
+                while (ok && p.next(a, b0, b1)) {
+                    const bool two = p.w.n_q * a.group - p.t * ROWS > TM;
+                    if (!(n & 1 ? open(T1{}, two) : open(T0{}, two))) break;
+                    for (int j = b0; j < b1; ++j)
+                        if (!(n & 1 ? step(T1{}, two, j == b0, j + 1 < b1) : step(T0{}, two, j == b0, j + 1 < b1))) break;
                 }
-            };
-            using T0 = std::integral_constant<int, 0>;
-            using T1 = std::integral_constant<int, 1>;
-            // scores of an item's first block (block n of this CTA, in half `st` of the ring)
-            auto open = [&](auto st, bool two) {
-                constexpr int h = decltype(st)::value;
-                if (!wait(tfull(2 * h), (n >> 1) & 1) || !wait(qfull(0), nq0++ & 1)) return false;
-                scores(T0{}, st);
-                if (two) {
-                    if (!wait(qfull(1), nq1++ & 1)) return false;
-                    scores(T1{}, st);
-                }
-                commit(tempty(2 * h));
-                return true;
-            };
-            // values of block n, scores of block n + 1 if the piece has it: tile 0, then tile 1
-            auto step = [&](auto st, bool two, bool first, bool more) {
-                constexpr int h = decltype(st)::value;
-                using Next = std::integral_constant<int, 1 - h>;
-                if (!wait(tfull(2 * h + 1), (n >> 1) & 1)) return false;
-                if (more && !wait(tfull(2 * (1 - h)), ((n + 1) >> 1) & 1)) return false;
-                if (!wait(pfull(0), np0++ & 1)) return false;
-                values(T0{}, st, first);
-                if (more)
-                    scores(T0{}, Next{});
-                else
-                    commit(ofull(0));
-                if (two) {
-                    if (!wait(pfull(1), np1++ & 1)) return false;
-                    values(T1{}, st, first);
-                    if (!more) commit(ofull(1));
-                }
-                commit(tempty(2 * h + 1));
-                if (more) {
-                    if (two) scores(T1{}, Next{});
-                    commit(tempty(2 * (1 - h)));
-                }
-                ++n;
-                return true;
-            };
-            while (ok && p.next(a, b0, b1)) {
-                const bool two = p.w.n_q * a.group - p.t * ROWS > TM;
-                if (!(n & 1 ? open(T1{}, two) : open(T0{}, two))) break;
-                for (int j = b0; j < b1; ++j)
-                    if (!(n & 1 ? step(T1{}, two, j == b0, j + 1 < b1) : step(T0{}, two, j == b0, j + 1 < b1))) break;
+                if (!ok) give_up();
             }
-            if (!ok && lane == 0) give_up();
             __syncwarp();
         }
     } else if (warp >= SOFT_WARPS) {
