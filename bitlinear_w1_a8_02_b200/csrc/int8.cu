@@ -215,7 +215,9 @@ cudaError_t launch_gemv(const Int8Args& a, const uint16_t* x, bool norm, cudaStr
 //
 // M > 128: TMA brings 128 bytes of K of 128 tokens and BN weight rows per stage, one thread issues tcgen05.mma kind::i8
 // into one of two int32 accumulators in TMEM, eight warps read the other one out. Persistent blocks take whole tiles;
-// weight tiles are shared by consecutive tiles.
+// weight tiles are shared by consecutive tiles. Bound by the tensor work: 2048 tokens 8192 -> 28672 341 us, 2.8 POP/s,
+// the tensor pipe 77% busy; where there is a tile or less to an SM, by the latency of its loads: 2560 -> 2560 with 300
+// tokens 11.2 us.
 constexpr int BM = 128, BK = 128;
 constexpr int A_BYTES = BM * BK;
 constexpr int EPI_WARPS = 8;  // two to a quarter of TMEM's lanes, 32 columns in turn
@@ -444,7 +446,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 // Bound by the weights' bytes, so every SM has to stream its share: a block takes 128 weight rows (the MMA's M) and the
 // tokens are its N, and where there are fewer tiles of 128 rows than SMs, the blocks of a cluster take a K range of one
 // tile each. Their int32 sums meet through distributed shared memory: each block finishes its share of the rows.
-// Weight loads start before the kernel waits for the one before it.
+// Weight loads start before the kernel waits for the one before it. 16 tokens 8192 -> 28672: 45 us with cold caches, 5.2
+// TB/s; 2560 -> 6912 7 us with the quantiser, most of it the two kernels' latencies.
 constexpr int FEW_MAX = 128;
 constexpr int FEW_EPI = 128, FEW_THREADS = 64 + FEW_EPI;
 constexpr int FEW_SMEM[3] = {55 * 1024, 74 * 1024, 104 * 1024};  // four, three, two blocks per SM
@@ -718,7 +721,19 @@ cudaError_t launch_pack_int8(const void* W, bool fp32, int64_t N, int64_t K, int
 }
 
 namespace {
-// 256 weight rows a tile unless narrower ones finish sooner: waves times the relative time of a tile.
+// 65 to 128 tokens: tiles of tokens (below) rather than of weights where these fill the SMs without a K split, or nearly
+// so with short rows. In us, tiles of weights against of tokens, 96 tokens: 2560 -> 6912 12.4 and 10.8, 2560 -> 13824
+// 15.0 and 12.4, 2560 -> 128256 74.9 and 63.5, 1024 -> 9000 10.1 and 8.3; 6912 -> 2560 12.9 and 19.1, 8192 -> 8192 19.9
+// and 24.1. With 33 tokens: 2560 -> 6912 9.6 and 12.6, 2560 -> 128256 56.9 and 70.5.
+bool many_rows(int64_t M, int64_t N, int64_t K, int sms) {
+    const int64_t tiles = (N + BM - 1) / BM;
+    return M > 64 && (tiles > sms || (3 * tiles >= sms && K <= 4096));
+}
+
+// 256 weight rows a tile unless narrower ones finish sooner: waves times the relative time of a tile. In us for 64, 128
+// and 256 rows: 2560 x 2560 with 300 tokens 11.2, 12.1, 14.6; 6912 x 2560 with 256 tokens 16.3, 12.9, 15.7; 8192 x
+// 8192 with 800 tokens 126, 78, 57. Of 63
+// shapes measured the pick was 9% off at worst (6919 x 2560 with 800 tokens).
 int int8_tile_width(int64_t M, int64_t N, int sms) {
     const int64_t mt = (M + BM - 1) / BM;
     const int width[3] = {256, 128, 64};
@@ -750,7 +765,7 @@ cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t
         if (e != cudaSuccess) return e;
         if (dev < 64) num_sms[dev] = sms;
     }
-    if (M <= FEW_MAX) return launch_few(a, sms, dev, s);
+    if (M <= FEW_MAX && !many_rows(M, N, K, sms)) return launch_few(a, sms, dev, s);
     switch (int8_tile_width(M, N, sms)) {
         case 64: return launch_gemm_bn<64>(a, sms, dev, s);
         case 128: return launch_gemm_bn<128>(a, sms, dev, s);
