@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 // TB/s; 2560 -> 6912 7 us with the quantiser, most of it the two kernels' latencies.
 constexpr int FEW_MAX = 128;
 constexpr int FEW_EPI = 128, FEW_THREADS = 64 + FEW_EPI;
-constexpr int FEW_SMEM[3] = {55 * 1024, 74 * 1024, 104 * 1024};  // four, three, two blocks per SM
+constexpr int FEW_SMEM = 104 * 1024, FEW_SMEM_TALL = 55 * 1024;  // two and four blocks per SM
 constexpr int FEW_STAGES_MAX = 6;
 
 struct FewArgs {
@@ -657,10 +657,9 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
         const int blocks = tiles << (f.log_split + 1), least = blocks <= sms ? 2 : std::min(2 + f.cols / 16, 6);
         if (blocks > 2 * sms || nkb < least << (f.log_split + 1)) break;
     }
-    // Deep rings where every block is resident; else as many blocks per SM as keep two stages (the sums need two), so
-    // that some load while others start or finish.
-    const int room = tiles <= 2 * sms ? 2 : 2 * stage + 1024 <= FEW_SMEM[0] ? 0 : 1;
-    f.stages = std::min(FEW_STAGES_MAX, (FEW_SMEM[room] - 1024) / stage);
+    // Deep rings where every block is resident; else (up to 64 tokens: many_rows takes the others) twice the blocks per SM with two stages or three,
+    // so that some load while others start or finish: 2560 -> 128256 with 2 tokens 57.3 -> 52.0 us, with 64 69.0 -> 61.8.
+    f.stages = std::min(FEW_STAGES_MAX, ((tiles <= 2 * sms ? FEW_SMEM : FEW_SMEM_TALL) - 1024) / stage);
     CUtensorMap mapW, mapX;
     if (!make_map(&mapW, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BM, BK, true) ||
         !make_map(&mapX, a.xq, (uint64_t)a.M, (uint64_t)a.K, (uint32_t)f.cols, BK, true))
@@ -670,7 +669,7 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     static bool attr_set[64];
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(few_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM[2]);
+        e = cudaFuncSetAttribute(few_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }

@@ -111,6 +111,28 @@ def test_forward(M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("N", [40001, 40004, 40008])
+@pytest.mark.parametrize("M", [1, 2, 16, 40, 64, 65, 100, 128, 150])
+def test_many_rows(M, N):
+    """More tiles of weights than the device holds at once; rows of every alignment, each kind of output."""
+    K = 208
+    Wq = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    step = torch.rand(N, device="cuda")
+    x = synth.activations(M, K, seed=M, outliers=True).cuda()
+    res = torch.randn(M, N, device="cuda").to(torch.bfloat16)
+    codes, s, _ = bl.quant_act(x)
+    acc = codes.double() @ Wq.double().t()
+    y = (acc.float() * step) * s.reciprocal()[:, None]
+    for residual in (None, res):
+        want = y if residual is None else residual.float() + y
+        got, ga = bl.forward_int8(Wq, step, x, residual=residual, want_acc=True)
+        assert torch.equal(ga.double(), acc) and torch.equal(got, want.to(torch.bfloat16))
+        assert torch.equal(bl.forward_int8(Wq, step, x, residual=residual), want.to(torch.bfloat16))
+        assert torch.equal(bl.forward_int8(Wq, step, x, residual=residual, out_dtype=torch.float32), want)
+    assert bl.get_device_error() == 0
+
+
+@gpu
 @pytest.mark.parametrize("M", [1, 2])
 @pytest.mark.parametrize("K", [4080, 4096, 4112, 32752, 32768, 40928, 40944, 131072])
 def test_lengths_around_the_kernel_choice(M, K):
