@@ -482,6 +482,21 @@ def test_attention_long_sequence(new):
 
 
 @gpu
+@pytest.mark.parametrize("new,heads,D", [(1, 1, 64), (1, 3, 128), (2, 4, 64), (5, 3, 128), (7, 3, 64), (5, 4, 128), (30, 4, 128), (43, 3, 64)])
+def test_few_rows_in_many_pieces(new, heads, D):
+    """One long sequence whose keys all blocks share, beside one that a single block holds."""
+    b = Batch([(new, 9001), (new, new + 3)], D, heads, 1, 64, seed=new)
+    n = 9001 + new + 3
+    k = b.rng.standard_normal((n, 1, D)).astype(np.float32)
+    k[:3000] *= 3  # maxima that differ from piece to piece
+    b.fill(k, b.rng.standard_normal((n, 1, D)).astype(np.float32))
+    q = torch.from_numpy(b.rng.standard_normal((b.M, heads, D))).to(torch.bfloat16).cuda()
+    out = bl.kv4_attention(q, *b.args(), new)
+    assert bl.get_device_error() == 0
+    b.check(q, out)
+
+
+@gpu
 def test_bad_batches_are_reported_and_stay_inside():
     """Every case is one that the kernels' own bounds checks catch."""
     BAD = 10
