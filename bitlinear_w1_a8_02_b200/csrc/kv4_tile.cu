@@ -17,7 +17,7 @@
 //                        work on the other.
 //   softmax   (2 x 4 warps) a thread owns a row: maximum, exponentials, denominator in
 //                        fp32; P goes back to TMEM over S as bf16. O is rescaled only when a
-//                        row's maximum grows by more than 2^8.
+//                        row's exponentials of a block sum up to more than 2^10.
 // Work split as in kv4_attn.cu: the units of all items in one line, an equal
 // contiguous range per CTA (one CTA per SM), pieces of split items joined by a
 // second kernel in a fixed order. Causal limits cut an item's blocks short.
@@ -680,8 +680,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     }
                 };
                 // Exponentials against the maximum so far. A row whose sum shows that its maximum has grown too much
-                // (always on the first block, and while no score was above -inf) has it raised, and the warp takes the pass again: the scores stay where
-                // they are until P is stored over them. Nothing else looks at the scores' maximum.
+                // (always on the first block, and while no score was above -inf) has it raised, and the warp takes the
+                // pass again: the scores stay where they are until P is stored over them. Nothing else looks at the
+                // scores' maximum.
                 float sum = 0.0f;
                 uint32_t pk[2][32];
                 for (bool again = b == b0;;) {
