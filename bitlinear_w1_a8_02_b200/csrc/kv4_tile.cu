@@ -212,6 +212,13 @@ __device__ __forceinline__ int warp_scan(int v) {  // inclusive
     return v;
 }
 
+// Whether q_start decreases at a sequence of group g. The host bounds the units by 2^31 from M rows in all; seq_of
+// checks a sequence for itself, but only sequences in order have rows of their own, which add up to M.
+__device__ __forceinline__ bool group_decreases(const TileArgs& a, int g) {
+    const int s = g * SEQ_GROUP + (int)(threadIdx.x & 31);
+    return __any_sync(0xffffffffu, s < a.batch.S && a.batch.q_start[s] > a.batch.q_start[s + 1]);
+}
+
 // Units of the SEQ_GROUP sequences of group g, sequence g * SEQ_GROUP + lane in each lane; the warp shares the
 // tiles of each long sequence.
 __device__ __forceinline__ int group_units(const TileArgs& a, int g, bool report) {
@@ -254,7 +261,7 @@ struct Pieces {
                         t = 0;
                         do {
                             w = seq_of(a, ++s, false);
-                        } while (w.tiles == 0);  // a later sequence has units: u < u1 <= total
+                        } while (w.tiles == 0);  // a later sequence has units: u < u1 <= total, and total is exact
                     }
                 }
                 blocks = blocks_of(a, w, t);
@@ -320,15 +327,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
     // ---- units of all sequences, and where this CTA's range of them starts
     const int groups = (a.batch.S + SEQ_GROUP - 1) / SEQ_GROUP;
     for (int g = warp; g < groups; g += THREADS / 32) {
-        const int sum = warp_sum(group_units(a, g, blockIdx.x == 0));
-        if (lane == 0) coarse[g + 1] = sum;
+        const bool decreases = group_decreases(a, g);
+        const int sum = decreases ? -1 : warp_sum(group_units(a, g, blockIdx.x == 0));
+        if (lane == 0) {
+            coarse[g + 1] = sum;
+            if (decreases && blockIdx.x == 0) atomicOr(a.err, kErrBadBatch);
+        }
     }
     __syncthreads();
     if (warp == 0) {
         int carry = 0;
         for (int g0 = 0; g0 < groups; g0 += 32) {
             const int g = g0 + lane;
-            const int sum = carry + warp_scan(g < groups ? coarse[g + 1] : 0);
+            const int own = g < groups ? coarse[g + 1] : 0;
+            if (__any_sync(0xffffffffu, own < 0)) {  // a batch out of order has no work; up to here its sums are sound
+                carry = 0;
+                break;
+            }
+            const int sum = carry + warp_scan(own);
             if (g < groups) coarse[g + 1] = sum;
             carry = __shfl_sync(0xffffffffu, sum, 31);
         }

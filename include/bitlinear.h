@@ -394,8 +394,10 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
  * tokens that a call appends must not share a slot.
  * The arrays live on the device, so their contents are checked by the kernels:
  * a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P, a
- * q_start that leaves 0 .. M, or a position past the rotation table sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
- * access leaves the buffers, and the rows concerned are unspecified.
+ * q_start that leaves 0 .. M or decreases, or a position past the rotation table
+ * sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
+ * access leaves the buffers, and the rows concerned (all rows of a batch whose
+ * q_start decreases) are unspecified.
  *
  * Sizes for all calls: D 64 or 128; P 16, 32, 64, 128 or 256; 1 <= S <= 4096;
  * Hq % Hkv == 0, Hq <= 1024; M <= 65535; W >= 1, W P < 2^30, S Hkv W P < 2^36;
