@@ -85,17 +85,17 @@ struct RowsSmem {
 // tc::mbar_wait with a hint that lets the warp sleep up to 20 us at a time: the polls of waiting warps take issue
 // slots from the unpacking ones.
 __device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = tc::globaltimer_ns();
-    do {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
-    } while (tc::globaltimer_ns() - t0 <= kWaitLimitNs);
-    return false;
+    return bounded_wait<1>(
+        [&] {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+            return ok != 0;
+        },
+        [] { return tc::globaltimer_ns(); }, kWaitLimitNs);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

@@ -9,6 +9,8 @@
 #include <cuda.h>  // CUtensorMap (type only)
 #include <stdint.h>
 
+#include "bounded.h"
+
 namespace bl {
 namespace tc {
 
@@ -54,14 +56,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Wait for phase `parity` to complete, giving up after `limit_ns` nanoseconds.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > limit_ns) return false;
-    }
+    return bounded_wait<32>([&] { return mbar_try_wait(bar, parity); }, [] { return globaltimer_ns(); }, limit_ns);
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
