@@ -130,6 +130,17 @@ __device__ __forceinline__ uint32_t raw_pair(uint32_t w) {
 
 constexpr int kSpacing = 133;  // -log2 of the spacing of bf16's subnormals
 
+// Barrier of the consumer warps that tells all of them whether any thread of theirs came with `p`.
+__device__ __forceinline__ bool consumers_meet(bool p) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)p), "n"(32 * kWarps)
+        : "memory");
+    return any != 0;
+}
+
 // Units of kKeys keys of sequence s (0 when it has no new tokens or was refused).
 struct SeqWork {
     int n_q, len, row0, blocks, row_blocks;
@@ -598,8 +609,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                     const int dim = 32 * (w % G) + 8 * (w / G) + n;
                     merge[(warp * RB + nt * 8 + 2 * t + (e & 1)) * D + dim] = o[nt][i][e];
                 }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-        if (*abort_flag) break;  // the same for the four warps: set before the barrier, and nothing sets it after
+        // The producer may set the flag at any time, so the warps leave by what they brought to the barrier, which is the
+        // same for all four: one that left while another went on to the next barrier would keep it there for good.
+        if (consumers_meet(!ok || *abort_flag)) break;
         const bool starts = begin == it.first, ends = end == it.end;
         const bool whole = starts && ends;
         float* slot = a.slots + (size_t)(2 * c + (starts ? 1 : 0)) * RB * (D + 2);
