@@ -53,7 +53,7 @@ constexpr int UNPACK_THREADS = 32 * UNPACK_WARPS;
 constexpr int EPI_THREADS = 128;
 constexpr int THREADS = 64 + UNPACK_THREADS + EPI_THREADS;  // TMA, MMA, unpack, epilogue warps
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
-constexpr int NUM_BARS = 2 * TSTAGES + 2 * USTAGES + 4;
+constexpr int NUM_BARS = 2 * TSTAGES + 2 * USTAGES + 5;
 
 // Sizes that follow from the tile width BN (weight rows per tile = TMEM columns
 // per accumulator): 256 normally, 128 or 64 when wider tiles cannot fill the SMs.
@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto uempty = [&](int u) { return bar(2 * TSTAGES + USTAGES + u); };     // MMA done with it
     auto afull = [&](int a) { return bar(2 * TSTAGES + 2 * USTAGES + a); };  // accumulator ready
     auto aempty = [&](int a) { return bar(2 * TSTAGES + 2 * USTAGES + 2 + a); };  // drained
+    const uint32_t teardown = bar(2 * TSTAGES + 2 * USTAGES + 4);  // last MMAs, after an abort
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int TN = DUAL ? BN / 2 : BN;  // output columns per tile
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_init(afull(a), 1);
             tc::mbar_init(aempty(a), EPI_THREADS);
         }
+        tc::mbar_init(teardown, 1);
         abort_sh = 0;
         tc::fence_mbar_init();
     }
@@ -489,9 +491,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         if (lane == 0 && abort_sh) {
-            // no MMA may still be writing TMEM when it is released
-            tc::mma_commit(afull(0));
-            tc::mbar_wait(afull(0), 0, WAIT_LIMIT_NS);
+            // no MMA may still be writing TMEM when it is released (a barrier of its own: the others have phases behind them)
+            tc::mma_commit(teardown);
+            tc::mbar_wait(teardown, 0, WAIT_LIMIT_NS);
         }
         __syncwarp();
         tc::fence_after_sync();

@@ -226,7 +226,7 @@ template <int BN>
 struct Gemm {
     static constexpr int B_BYTES = BN * BK;
     static constexpr int STAGES = BN == 256 ? 4 : 6;
-    static constexpr int BARS = 2 * STAGES + 4;
+    static constexpr int BARS = 2 * STAGES + 5;
     static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + BARS * 8;
     static_assert(SMEM + EPI_WARPS * 4 * (16 * 33 + BN) + 16 <= 227 * 1024, "shared memory of a block");
 };
@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     auto empty = [&](int i) { return tc::smem_u32(bars + STAGES + i); };
     auto afull = [&](int i) { return tc::smem_u32(bars + 2 * STAGES + i); };
     auto aempty = [&](int i) { return tc::smem_u32(bars + 2 * STAGES + 2 + i); };
+    const uint32_t drained = tc::smem_u32(bars + 2 * STAGES + 4);  // teardown after an abort
     volatile int* aborted = &abort_sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_tiles = (a.N + BN - 1) / BN, m_tiles = (a.M + BM - 1) / BM;
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) tc::mbar_init(full(i), 1), tc::mbar_init(empty(i), 1);
         for (int i = 0; i < 2; ++i) tc::mbar_init(afull(i), 1), tc::mbar_init(aempty(i), 32 * EPI_WARPS);
+        tc::mbar_init(drained, 1);
         abort_sh = 0;
         tc::fence_mbar_init();
     }
@@ -431,9 +433,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         if (lane == 0 && abort_sh) {
-            // no MMA may still be writing TMEM when it is released
-            tc::mma_commit(afull(0));
-            tc::mbar_wait(afull(0), 0, WAIT_LIMIT_NS);
+            // no MMA may still be writing TMEM when it is released (a barrier of its own: the others have phases behind them)
+            tc::mma_commit(drained);
+            tc::mbar_wait(drained, 0, WAIT_LIMIT_NS);
         }
         __syncwarp();
         tc::fence_after_sync();
