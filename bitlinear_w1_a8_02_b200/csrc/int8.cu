@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     tc::tma_load_2d(tc::smem_u32(sB + s * B_BYTES), &tmB, kb * BK, n0, full(s));
                 }
             }
-            if (*aborted)  // let the copies still in flight land before the CTA exits
-                for (uint32_t h = g > STAGES ? g - STAGES : 0; h < g; ++h)
-                    tc::mbar_wait(full(h % STAGES), (h / STAGES) & 1, WAIT_LIMIT_NS);
+            // let the copies still in flight land before the CTA exits: the MMA thread waits for them too, unless it gives up
+            for (uint32_t h = g > STAGES ? g - STAGES : 0; h < g; ++h)
+                tc::mbar_wait(full(h % STAGES), (h / STAGES) & 1, WAIT_LIMIT_NS);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(FEW_THREADS)
                 weights(kb, s);
                 tokens(kb, s);
             }
-            if (*aborted)  // let the copies still in flight land before the block exits
-                for (int h = max(0, g - f.stages); h < g; ++h) tc::mbar_wait(full(h % f.stages), (h / f.stages) & 1, WAIT_LIMIT_NS);
+            // let the copies still in flight land before the block exits, as above
+            for (int h = max(0, g - f.stages); h < g; ++h) tc::mbar_wait(full(h % f.stages), (h / f.stages) & 1, WAIT_LIMIT_NS);
         }
     } else if (warp == 1) {
         grid_dependency_wait();

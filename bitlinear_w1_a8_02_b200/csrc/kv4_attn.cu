@@ -308,14 +308,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 }
             }
         }
-        if (!ok) {
-            if (lane == 0) {
+        if (lane == 0) {
+            if (!ok) {
                 atomicOr(a.err, kErrTimeout);
                 *abort_flag = 1;
-                // let the copies still in flight land before the CTA exits
-                for (int h = max(0, g - kStages); h < g; ++h)
-                    tc::mbar_wait(full(h % kStages), (h / kStages) & 1, kWaitLimitNs);
             }
+            // let the copies still in flight land before the CTA exits: the consumers wait for them too, unless they give up
+            for (int h = max(0, g - kStages); h < g; ++h) mbar_wait_asleep(full(h % kStages), (h / kStages) & 1);
         }
         return;
     }

@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                     }
                 }
             }
+            bool told = false;
             if (ok) {  // tell the unpackers that this was all
                 const int st = g % CODE_STAGES;
                 if (g >= CODE_STAGES) ok = tc::mbar_wait(cempty(st), (g / CODE_STAGES - 1) & 1, WAIT_NS);
@@ -465,12 +466,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 if (ok && lane == 0) {
                     valid_sh[st] = -1;
                     tc::mbar_arrive(cfull(st));
+                    told = true;
                 }
             }
-            if (!ok && lane == 0) {
-                give_up();
-                // let the copies still in flight land before the CTA exits
-                for (uint32_t h = g > CODE_STAGES ? g - CODE_STAGES : 0; h < g; ++h)
+            if (lane == 0) {
+                if (!ok) give_up();
+                // Let the copies still in flight land before the CTA exits: the unpackers wait for them too, unless they
+                // give up. The stage whose barrier told them the end was empty, so its copies have landed.
+                for (uint32_t h = g >= CODE_STAGES ? g - CODE_STAGES + (told ? 1 : 0) : 0; h < g; ++h)
                     tc::mbar_wait(cfull(h % CODE_STAGES), (h / CODE_STAGES) & 1, WAIT_NS);
             }
         } else if (warp == MMA_WARP) {

@@ -29,3 +29,40 @@ def test_last_products_are_waited_for_on_a_barrier_of_their_own():
         fresh.complete()  # the commit comes
         assert fresh.passes(0)
     assert early == [False, True, False, True, False, True]
+
+
+def drain(first, g, stages):
+    """(stage, parity) of the waits of the loading thread for the units first .. g - 1."""
+    return [(h % stages, h // stages & 1) for h in range(first, g)]
+
+
+def ring(stages, g, landed, end_marker):
+    """The stages' barriers after `g` units, those below `landed` being there, and with the marker that tells the end."""
+    bars = [Barrier() for _ in range(stages)]
+    for h in range(landed):
+        bars[h % stages].complete()
+    if end_marker:
+        bars[g % stages].complete()
+    return bars
+
+
+def test_copies_in_flight_are_waited_for_whoever_gave_up():
+    """The loading thread may have issued its last copy before a consumer gives up. Whatever is still in flight then, its
+    waits do not all pass, and once it has landed they all do, also where the stage after the last unit has served to
+    tell the end (the unit that it held before was consumed)."""
+    for stages in range(1, 7):
+        for g in range(0, 4 * stages + 2):
+            for told in (False, True):
+                first = g - stages + (1 if told else 0) if g >= stages else 0
+                for landed in range(first, g + 1):
+                    bars = ring(stages, g, landed, told)
+                    passes = all(bars[s].passes(p) for s, p in drain(first, g, stages))
+                    assert passes == (landed == g), (stages, g, told, landed)
+
+
+def test_the_stage_that_told_the_end_is_not_waited_for():
+    """Its barrier is a phase further: a wait for the unit that it held would not pass any more."""
+    for stages in range(1, 7):
+        g = 3 * stages + 1
+        bars = ring(stages, g, g, True)
+        assert not all(bars[s].passes(p) for s, p in drain(g - stages, g, stages))
