@@ -634,6 +634,8 @@ bl_status rows_ok(const uint16_t* p, int64_t stride, int64_t width) {
     return BL_OK;
 }
 
+constexpr float kScaleMin = 7.888609052210118e-31f, kScaleMax = 1.2676506002282294e30f;  // 2^-100, 2^100
+
 inline bool heads_ok(int32_t Hq, int32_t hkv) { return Hq >= 1 && Hq <= 1024 && Hq % hkv == 0; }
 
 }  // namespace
@@ -679,7 +681,7 @@ BL_API bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, in
     bl::Kv4View view;
     bl::Kv4Seqs seqs;
     if (bl_status st = kv4_args(cache, batch, M, &view, &seqs)) return st;
-    if (!heads_ok(Hq, cache->kv_heads) || max_q < 0 || !(scale > 0.0f && scale <= 3.0e38f)) return BL_ERR_SHAPE;
+    if (!heads_ok(Hq, cache->kv_heads) || max_q < 0 || !(scale >= kScaleMin && scale <= kScaleMax)) return BL_ERR_SHAPE;
     // units of work (blocks of keys x items of rows) are counted in 32 bits
     const int64_t room = (int64_t)batch->W * cache->page_size;
     if ((M * Hq / 256 + (int64_t)batch->S * cache->kv_heads) * (room / 128 + 8) >= (int64_t)1 << 31) return BL_ERR_SHAPE;

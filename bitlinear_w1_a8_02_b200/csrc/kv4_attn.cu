@@ -35,6 +35,7 @@
 #include <algorithm>
 
 #include <cfloat>
+#include <cmath>
 
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
@@ -62,6 +63,7 @@ struct RowsArgs {
     Kv4Seqs batch;
     int M, group, max_q;  // query heads per key/value head
     float scale_log2;     // scale * log2(e)
+    int least_shift;      // of the queries' scaling, so that scale_log2 * 2^(kSpacing - shift) stays below 2^127
     float* slots;         // [2 gridDim.x][8 NT][D + 2]: sums, maximum, denominator of pieces
     int4* joins;          // [gridDim.x]: item whose first piece the CTA holds (see JoinItem), or .w = -1
     unsigned* err;
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             top = max(top & 0xFFFFu, top >> 16);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int shift = min(127, max(10, 227 - (int)(top >> 7)));
+            const int shift = min(127, max(a.least_shift, 227 - (int)(top >> 7)));
             const uint32_t even = (uint32_t)(127 + shift) << 7, odd = (uint32_t)(123 + shift) << 7;
             const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
 #pragma unroll
@@ -787,6 +789,7 @@ cudaError_t launch_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M,
     a.cache = cache, a.batch = batch;
     a.M = (int)M, a.group = Hq / cache.hkv, a.max_q = (int)std::min<int64_t>(max_q, M);
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.least_shift = std::max(10, kSpacing - 127 + 1 + std::ilogb(a.scale_log2) + 1);
     a.slots = (float*)ws;
     a.joins = (int4*)((char*)ws + rows_slots_bytes(D));
     cudaError_t e = device_error_word(&a.err);

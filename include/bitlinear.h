@@ -459,13 +459,13 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j - max)),  j <= position
  * on the values that the cache holds; products and sums in fp32, p_j rounded to
  * bf16 for the product with v_j. A row that sees no key is zero. A query with a
- * NaN or an infinity makes its row NaN in that head; queries of magnitude 2^100 or
- * more may do so too. (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
+ * NaN or an infinity makes its row NaN in that head; queries of magnitude
+ * 2^100 / max(1, scale) or more may do so too. (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
  *   q, out      [M, Hq, D] device bf16, rows q_stride / out_stride elements apart;
  *               16-byte aligned, strides multiples of 8; must not overlap
  *   max_q       the largest number of new tokens of a sequence (host): a sequence
  *               with more is reported as BL_ERR_BAD_BATCH and left out
- *   scale       finite, > 0 (commonly 1 / sqrt(D))
+ *   scale       2^-100 .. 2^100 (commonly 1 / sqrt(D))
  *   ws          bitlinear_workspace_bytes(BL_OP_KV4_ATTENTION, max_q, Hq / Hkv, D) bytes
  * Deterministic: the same inputs give the same bits.
  */
