@@ -16,7 +16,10 @@
 //            multiply-add give the bf16 pair exactly (see kv4.cuh); P^T comes from the
 //            score registers by an 8x8 transpose.
 // A running maximum is kept per row and only raised when a score passes it by
-// 2^8 (in the exponent's base-2 units), so accumulators are rarely rescaled.
+// 2^8 (in the exponent's base-2 units), so accumulators are rarely rescaled. It is
+// taken off the scores before they are scaled: one multiply-add with the scaled
+// maximum would leave that one's rounding, which passes the exponent's range for
+// scores of 2^31 and more.
 //
 // Work split: all (sequence, head, row block) items are cut into units of 128
 // keys and every CTA takes one contiguous range of units, whatever the lengths
@@ -131,6 +134,10 @@ __device__ __forceinline__ uint32_t raw_pair(uint32_t w) {
 }
 
 constexpr int kSpacing = 133;  // -log2 of the spacing of bf16's subnormals
+
+// A maximum in the exponent's units. Below fp32 it weighs nothing, but is no NaN; above, the infinity makes its row NaN
+// where pieces meet.
+__device__ __forceinline__ float in_units(float m, float sc) { return fmaxf(m * sc, -FLT_MAX); }
 
 // Barrier of the consumer warps that tells all of them whether any thread of theirs came with `p`.
 __device__ __forceinline__ bool consumers_meet(bool p) {
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
         const int least = it.w.len - it.w.n_q + (it.rb * RB) / a.group + 1;  // keys every row sees
 
         float o[NT][MT][4];
-        float mx[NT][2], thr[NT][2], msc[NT][2], den[NT][2];
+        float mx[NT][2], thr[NT][2], ref[NT][2], den[NT][2];  // ref: the maximum, 0 while there is none
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) mx[nt][e] = thr[nt][e] = -INFINITY, msc[nt][e] = den[nt][e] = 0.0f;
+            for (int e = 0; e < 2; ++e) mx[nt][e] = thr[nt][e] = -INFINITY, ref[nt][e] = den[nt][e] = 0.0f;
         }
 
         bool ok = true;
@@ -489,11 +496,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                         m = fmaxf(m, mx[nt][e]);
-                        // a score may lie beyond fp32 where it is taken in binary units: then it weighs nothing, but is no NaN
-                        const float now = m == -INFINITY ? 0.0f : fmaxf(m * sc[nt][e], -FLT_MAX);
-                        const float f = exp2_approx(mx[nt][e] == -INFINITY ? -INFINITY : msc[nt][e] - now);
+                        const float f = exp2_approx(mx[nt][e] == -INFINITY ? -INFINITY : in_units(mx[nt][e], sc[nt][e]) - in_units(m, sc[nt][e]));
                         mx[nt][e] = m;
-                        msc[nt][e] = now;
+                        ref[nt][e] = m == -INFINITY ? 0.0f : m;
                         thr[nt][e] = m + kRaise / sc[nt][e];
                         den[nt][e] *= f;
 #pragma unroll
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(fmaf(sv[nt][e], sc[nt][e & 1], -msc[nt][e & 1]));
+                for (int e = 0; e < 4; ++e) p[e] = exp2_approx((sv[nt][e] - ref[nt][e & 1]) * sc[nt][e & 1]);
                 den[nt][0] += p[0] + p[2];
                 den[nt][1] += p[1] + p[3];
                 pf[nt][0] = transpose8x8(pack_bf16(p[0], p[1]));
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 d += __shfl_xor_sync(0xffffffffu, d, 8);
                 d += __shfl_xor_sync(0xffffffffu, d, 16);
                 if (r == 0) {
-                    stats[(warp * RB + nt * 8 + 2 * t + e) * 2] = mx[nt][e] == -INFINITY ? -INFINITY : msc[nt][e];
+                    stats[(warp * RB + nt * 8 + 2 * t + e) * 2] = mx[nt][e] == -INFINITY ? -INFINITY : in_units(mx[nt][e], sc[nt][e]);
                     stats[(warp * RB + nt * 8 + 2 * t + e) * 2 + 1] = d;
                 }
             }

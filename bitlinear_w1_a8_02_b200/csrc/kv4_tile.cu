@@ -60,6 +60,7 @@ constexpr int MAX_CTAS = 148;     // sizes the workspace
 constexpr int ITEM_UNITS = 4;
 constexpr int SEQ_GROUP = 32;     // sequences per entry of the coarse unit table
 constexpr uint64_t WAIT_NS = 1000000000ull;
+constexpr float FAR = 16777216.0f;    // scaled maximum whose rounding is one in the exponent
 constexpr float RAISE_SUM = 1024.0f;  // sum of a row's exponentials over a block that raises its maximum
 
 struct TileArgs {
@@ -682,6 +683,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(qfull(i));
             float mx = -INFINITY, msc = 0.0f, den = 0.0f;
+            bool some_far = false;  // of the warp's rows
             for (int b = b0; b < b1; ++b, ++ns) {
                 ok = !*aborted && tc::mbar_wait(sfull(i), ns & 1, WAIT_NS);
                 ok = __all_sync(0xffffffffu, ok);
@@ -704,7 +706,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 // scores' maximum.
                 float sum = 0.0f;
                 uint32_t pk[2][32];
-                for (bool again = b == b0;;) {
+                // A row whose scaled maximum is far from zero has the maximum itself taken off its scores, once it holds for
+                // the block: the rounding of the scaled one, which the multiply-add leaves in every exponent, would pass the
+                // exponent's range from 2^31 on.
+                for (bool again = b == b0 || some_far;;) {
                     if (again) {
                         float m = -INFINITY;
                         load(0);
@@ -719,11 +724,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                         }
                         float f = 1.0f;
                         if (m > mx) {
-                            const float now = fmaxf(m * sc, -FLT_MAX);  // a score beyond fp32 weighs nothing, but is no NaN
+                            const float now = fmaxf(m * sc, -FLT_MAX);  // a score below fp32 weighs nothing, but is no NaN
                             f = mx == -INFINITY ? 0.0f : exp2_approx(msc - now);
                             mx = m;
                             msc = now;
-                            den *= f;
+                            den = now > FLT_MAX ? NAN : den * f;  // above fp32: no softmax
+                        }
+                        some_far = __any_sync(0xffffffffu, fabsf(msc) >= FAR);
+                        if (some_far) {
+                            const float take = fabsf(msc) >= FAR ? mx : 0.0f;
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                tc::tmem_ld_32x32(tS + 32 * k, s[0]);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[0][x] = __float_as_uint(__uint_as_float(s[0][x]) - take);
+                                tc::tmem_st_32x32(tS + 32 * k, s[0]);
+                            }
+                            tc::tmem_st_wait();
                         }
                         if (b > b0) {  // the block before has been added: its MMA finished before this S
 #pragma unroll 1
@@ -736,7 +754,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                             }
                         }
                     }
-                    const float2 sc2 = make_float2(sc, sc), off2 = make_float2(-msc, -msc);
+                    const float off = fabsf(msc) >= FAR ? 0.0f : -msc;
+                    const float2 sc2 = make_float2(sc, sc), off2 = make_float2(off, off);
                     uint32_t top = 0;  // bits of exp2_poly's sums
                     float2 d2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     load(0);

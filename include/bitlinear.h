@@ -459,8 +459,10 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j - max)),  j <= position
  * on the values that the cache holds; products and sums in fp32, p_j rounded to
  * bf16 for the product with v_j. A row that sees no key is zero. A query with a
- * NaN or an infinity makes its row NaN in that head; queries of magnitude
- * 2^100 / max(1, scale) or more may do so too. (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
+ * NaN or an infinity makes its row NaN in that head, and so does a visible key with
+ * scale q . k log2(e) above fp32's range; one with q . k above it, and queries of
+ * magnitude 2^100 / max(1, scale) or more, may. A key whose score lies below that
+ * range weighs nothing beside others. (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
  *   q, out      [M, Hq, D] device bf16, rows q_stride / out_stride elements apart;
  *               16-byte aligned, strides multiples of 8; must not overlap
  *   max_q       the largest number of new tokens of a sequence (host): a sequence
