@@ -23,7 +23,8 @@ namespace {
 constexpr int kPackThreads = 256;
 constexpr float kWeightFloor = 1e-30f;
 
-// One CTA per weight row: absmax, then codes of 4 columns per thread.
+// One CTA per weight row: absmax, then codes of 4 columns per thread. A NaN, which a maximum passes over, becomes the
+// row's step; the codes are zero then, as with an infinite step.
 template <bool FP32>
 __global__ void __launch_bounds__(kPackThreads) pack_int8_kernel(const void* W, int K, int8_t* Wq, float* wstep) {
     __shared__ float scratch[kPackThreads / 32];
@@ -39,13 +40,17 @@ __global__ void __launch_bounds__(kPackThreads) pack_int8_kernel(const void* W, 
         }
     };
     float top = 0.0f, f[4];
+    bool nan = false;
     for (int c = threadIdx.x; c < K / 4; c += kPackThreads) {
         load4(c, f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(f[e]));
+        for (int e = 0; e < 4; ++e) {
+            top = fmaxf(top, fabsf(f[e]));
+            nan |= f[e] != f[e];
+        }
     }
     top = block_max<kPackThreads / 32>(top, scratch);
-    const float step = __fdiv_rn(fmaxf(top, kWeightFloor), 127.0f);
+    const float step = __syncthreads_or(nan) ? NAN : __fdiv_rn(fmaxf(top, kWeightFloor), 127.0f);
     for (int c = threadIdx.x; c < K / 4; c += kPackThreads) {
         load4(c, f);
         uint32_t w = 0;

@@ -482,6 +482,8 @@ bl_status bitlinear_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t M
  * "Method Adaptation": per-token absmax to 8-bit integers).
  *   wstep[n]   = fl(max(max_k |W[n, k]|, 1e-30) / 127)
  *   Wq[n, k]   = clip(rint(fl(W[n, k] / wstep[n])), -127, 127)
+ * A row with a NaN or an infinity has it as its step and zeros as its codes, so its
+ * outputs are NaN.
  * W [N, K] bf16 or fp32 as bitlinear_pack_weights (16-byte aligned), but K % 16 == 0;
  * Wq [N, K] int8, 16-byte aligned; wstep [N] fp32.
  */
