@@ -752,13 +752,22 @@ int int8_tile_width(int64_t M, int64_t N, int sms) {
     }
     return width[best];
 }
+
+// Whether n bytes at a and m at b have any in common.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
 }  // namespace
 
 cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x, bool rmsnorm,
                         int8_t* xq, float* scale, int64_t M, const uint16_t* residual, uint16_t* y16, float* y32, int32_t* acc,
                         cudaStream_t s) {
     Int8Args a{Wq, wstep, xq, scale, residual, y16, y32, acc, (int)M, (int)N, (int)K};
-    if (M == 1 && K <= kGemvMaxK && (N <= kGemvRows || N <= kGemvRatio * K)) return launch_gemv(a, x, rmsnorm, s);
+    // the one-token kernel's blocks read x while others already write, so an output in x's place takes the other kernels,
+    // which have x quantised before they start
+    const bool in_place = overlap(x, 2 * K, y16, 2 * N) || overlap(x, 2 * K, y32, 4 * N) || overlap(x, 2 * K, acc, 4 * N);
+    if (M == 1 && K <= kGemvMaxK && (N <= kGemvRows || N <= kGemvRatio * K) && !in_place) return launch_gemv(a, x, rmsnorm, s);
     cudaError_t e = launch_act_quant(x, M, K, XQ_NATURAL, xq, scale, nullptr, s, rmsnorm);
     if (e != cudaSuccess) return e;
     int dev = 0;

@@ -499,7 +499,7 @@ bl_status bitlinear_pack_weights_int8(const void* W, int wdt, int64_t N, int64_t
  *   Wq        [N, K] device int8, 16-byte aligned; N >= 0, K >= 16, K % 16 == 0
  *   x         [M, K] device bf16, 16-byte aligned; 0 <= M <= 65535
  *   residual  [M, N] device bf16, may be NULL; acc [M, N] device int32, may be NULL
- *   y         [M, N], contiguous
+ *   y         [M, N], contiguous; may be x or residual (an update in place)
  *   ws        bitlinear_workspace_bytes(BL_OP_FORWARD_INT8, M, N, K) bytes
  */
 bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x,

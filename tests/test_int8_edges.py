@@ -80,3 +80,31 @@ def test_a_row_does_not_depend_on_how_many_there_are(N, K, rmsnorm):
                 assert torch.equal(y[m:m + 1].view(torch.int16), alone.view(torch.int16)), (M, m)
         rest = [m for m in range(M) if m not in at]
         assert torch.equal(y[rest], plain[rest])
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 2, 17, 100, 300])
+@pytest.mark.parametrize("K", [512, 2560, 8192])
+def test_update_in_place(M, K):
+    """x, the residual and the output one tensor (h += layer(h)), and an output that overlaps part of x; with another stream
+    at work, so that some blocks start late."""
+    Wq = torch.randint(-127, 128, (K, K), dtype=torch.int8, device="cuda")
+    step = torch.rand(K, device="cuda") * 1e-4
+    x = synth.activations(M, K, seed=K, outliers=True).cuda()
+    side, a = torch.cuda.Stream(), torch.ones((4096, 4096), dtype=torch.bfloat16, device="cuda")
+    for norm in (False, True):
+        want = bl.forward_int8(Wq, step, x, rmsnorm=norm, residual=x)
+        copies = [x.clone() for _ in range(50)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                a @ a
+        for h in copies:
+            assert bl.forward_int8(Wq, step, h, rmsnorm=norm, residual=h, out=h) is h
+        torch.cuda.synchronize()
+        assert all(torch.equal(h, want) for h in copies)
+    if M == 1:
+        buf = torch.empty(2 * K, dtype=torch.bfloat16, device="cuda")
+        buf[:K] = x[0]
+        want = bl.forward_int8(Wq, step, x)
+        assert torch.equal(bl.forward_int8(Wq, step, buf[:K].view(1, K), out=buf[K // 2:K // 2 + K].view(1, K)), want)
