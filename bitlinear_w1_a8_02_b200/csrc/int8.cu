@@ -7,10 +7,14 @@
 // DRAM straight into int8 mma.sync fragments (m16n8k32, weights as A): a lane's 16
 // bytes of a row are the four words of two MMAs, and the lane's 16 bytes of the
 // token's codes line up with them, so neither side is rearranged. The token is
-// quantised inside the kernel, by every block for itself: one launch, 4.2 us
-// against 5.5 with a quantiser before the kernel for few tokens (2560 x
-// 2560). 100003 x 2560 with the
-// norm takes 43.6 us, 5.9 TB/s of weights and outputs.
+// quantised inside the kernel, by every block for itself: one launch, 4.1 us
+// against 5.5 with a quantiser before the kernel for few tokens (2560 x 2560).
+// 28672 x 8192 takes 43.6 us in a replayed graph, 5.4 TB/s of weights, 49 with
+// cold caches.
+//
+// Packing: a block a row, read twice (the second time from L2). Bound by the
+// codes' divisions: 128256 x 2560 410 us from bf16, 418 from fp32, 2.4 and 3.9
+// TB/s of weights and codes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -664,8 +668,9 @@ cudaError_t launch_few(const Int8Args& a, int sms, int dev, cudaStream_t s) {
         const int blocks = tiles << (f.log_split + 1), least = blocks <= sms ? 2 : std::min(2 + f.cols / 16, 6);
         if (blocks > 2 * sms || nkb < least << (f.log_split + 1)) break;
     }
-    // Deep rings where every block is resident; else (up to 64 tokens: many_rows takes the others) twice the blocks per SM with two stages or three,
-    // so that some load while others start or finish: 2560 -> 128256 with 2 tokens 57.3 -> 52.0 us, with 64 69.0 -> 61.8.
+    // Deep rings where every block is resident; else (up to 64 tokens: many_rows takes the others) twice the blocks per SM
+    // with two stages or three, so that some load while others start or finish: 2560 -> 128256 with 2 tokens 57.3 -> 52.0 us,
+    // with 64 69.0 -> 61.8.
     f.stages = std::min(FEW_STAGES_MAX, ((tiles <= 2 * sms ? FEW_SMEM : FEW_SMEM_TALL) - 1024) / stage);
     CUtensorMap mapW, mapX;
     if (!make_map(&mapW, a.Wq, (uint64_t)a.N, (uint64_t)a.K, BM, BK, true) ||
@@ -738,8 +743,7 @@ bool many_rows(int64_t M, int64_t N, int64_t K, int sms) {
 
 // 256 weight rows a tile unless narrower ones finish sooner: waves times the relative time of a tile. In us for 64, 128
 // and 256 rows: 2560 x 2560 with 300 tokens 11.2, 12.1, 14.6; 6912 x 2560 with 256 tokens 16.3, 12.9, 15.7; 8192 x
-// 8192 with 800 tokens 126, 78, 57. Of 63
-// shapes measured the pick was 9% off at worst (6919 x 2560 with 800 tokens).
+// 8192 with 800 tokens 126, 78, 57. Of 63 shapes measured the pick was 9% off at worst (6919 x 2560 with 800 tokens).
 int int8_tile_width(int64_t M, int64_t N, int sms) {
     const int64_t mt = (M + BM - 1) / BM;
     const int width[3] = {256, 128, 64};

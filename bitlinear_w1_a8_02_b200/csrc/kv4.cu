@@ -7,8 +7,8 @@
 // token with a non-finite value are warp shuffles and a ballot. A lane's 8 codes
 // are one 32-bit word of the packed vector.
 //
-// Bound by DRAM: per token 2 (Hq + 2 Hkv) D bytes in, 2 Hq D + Hkv (D + D/8) out;
-// the rotation row (4 D bytes) is read by every head of a token, so from L1.
+// Per token 2 (Hq + 2 Hkv) D bytes in, 2 Hq D + Hkv (D + D/8) out; the rotation
+// row (4 D bytes) is read by every head of a token, so from L1.
 // Measured (20 query, 5 key/value heads of 128): 6 x 2048 tokens 44.8 us with cold
 // caches, 3.9 TB/s of rows and codes, 80% of the issue slots: the quantisation's
 // arithmetic is the bound above a few thousand tokens, two dependent look-ups (the

@@ -29,10 +29,16 @@
 // each; a fifth copies the units' pages into a ring (bulk copies, the page ids
 // of 32 copies ahead loaded at once).
 //
-// Measured (20 query, 5 key/value heads of 128): 64 sequences of 8192 keys 100 us with
-// cold caches, 3.8 TB/s of cache, 57% of the issue slots; a copy without the loads takes
-// as long, so what bounds it is unpacking (55% of the ALU's slots). 64 sequences of 2048
-// keys: 35 us with 5 rows a head, 55 with 16. One sequence of 4001 keys: 9.9 us, units
+// The weights p_j are rounded to bf16 for the product with the values (2^-8 each, which
+// averages out over the keys): the tensor cores take no wider operand beside bf16 values.
+// The denominator sums them as they are.
+//
+// Measured (20 query, 5 key/value heads of 128): 64 sequences of 8192 keys 101 us with
+// cold caches, 3.7 TB/s of cache, 57% of the issue slots, 55% of the ALU's. A copy without
+// the loads takes as long, so memory is not the bound; neither pipe is full, so what bounds
+// it is the chain of a warp's 16 keys (scores, vote, exponentials, transpose, values) with
+// only 12 warps on an SM to hide it, 8 with more than 8 rows. 64 sequences of 2048
+// keys: 36 us with 5 rows a head, 55 with 16. One sequence of 4001 keys: 10.1 us, units
 // and joins about half each. Other splits measured slower: 8 warps a block, 3 stages,
 // 4 blocks an SM.
 #include <algorithm>
@@ -68,7 +74,7 @@ struct RowsArgs {
     float scale_log2;     // scale * log2(e)
     int least_shift;      // of the queries' scaling, so that scale_log2 * 2^(kSpacing - shift) stays below 2^127
     float* slots;         // [2 gridDim.x][8 NT][D + 2]: sums, maximum, denominator of pieces
-    int4* joins;          // [gridDim.x]: item whose first piece the CTA holds (see JoinItem), or .w = -1
+    int4* joins;          // [gridDim.x]: item whose first piece the CTA holds: first row, head, row block | rows << 24, last CTA; .w = -1: none
     unsigned* err;
 };
 

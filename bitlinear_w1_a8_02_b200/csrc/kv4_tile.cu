@@ -22,12 +22,17 @@
 // contiguous range per CTA (one CTA per SM), pieces of split items joined by a
 // second kernel in a fixed order. Causal limits cut an item's blocks short.
 //
-// Bound by the softmax and the tensor work that take turns: 2047 tokens on 30001 keys
-// (20 query, 5 key/value heads of 128) 535 us at 1.9 GHz, 1135 TFLOP/s, the tensor pipe
-// 52% busy, special functions 40%, issue slots 56%; six prompts of 100 to 4096 tokens
-// 187 us, a third of it the starts and ends of items. Without the softmax the former
-// takes 0.72 of the time. Pieces of one tile take as long a block as two; letting both
-// warpgroups share the blocks of one gained 3% there and cost 8% elsewhere.
+// The weights are rounded to bf16 for the product with the values; the denominator sums
+// them as they are.
+//
+// Measured (20 query, 5 key/value heads of 128): 2047 tokens on 30001 keys 528 us in a
+// burst, 1150 TFLOP/s, 596 sustained, 1019; the tensor pipe 53% busy, special functions
+// 40%, issue slots 57%. Six prompts of 100 to 4096 tokens 186 us, a third of it the starts
+// and ends of items. No pipe is full: timing copies at 2048 tokens on 16384 keys took 291
+// us whole, 209 without the softmax, 265 with one MMA of eight, 179 with neither, so the
+// larger part is unpacking and the hand-overs between the roles. Pieces of one tile take
+// as long a block as two; letting both warpgroups share the blocks of one gained 3% there
+// and cost 8% elsewhere.
 //
 // Every wait is bounded (1 s); one that gives up sets the device error word,
 // lets the CTA drain and returns.
@@ -767,7 +772,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             float2 e = fma2(make_float2(__uint_as_float(s[k & 1][2 * x]), __uint_as_float(s[k & 1][2 * x + 1])), sc2, off2);
-                            if (POLY_EVERY && x % (POLY_EVERY + !POLY_EVERY) == POLY_EVERY - 1) {
+                            if (x % POLY_EVERY == POLY_EVERY - 1) {
                                 e = exp2_poly(e, top);
                             } else {
                                 e.x = exp2_approx(e.x);
