@@ -62,6 +62,7 @@ constexpr int kItemUnits = 2;
 constexpr int kStages = 2;
 constexpr int kMaxCtas = 592;    // four per SM on 148 SMs; sizes the workspace
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr int kGaveUp = -2;
 constexpr float kRaise = 8.0f;   // a maximum is raised when a score passes it by this (base 2)
 
 struct RowsArgs {
@@ -74,7 +75,8 @@ struct RowsArgs {
     float scale_log2;     // scale * log2(e)
     int least_shift;      // of the queries' scaling, so that scale_log2 * 2^(kSpacing - shift) stays below 2^127
     float* slots;         // [2 gridDim.x][8 NT][D + 2]: sums, maximum, denominator of pieces
-    int4* joins;          // [gridDim.x]: item whose first piece the CTA holds: first row, head, row block | rows << 24, last CTA; .w = -1: none
+    int4* joins;          // [gridDim.x]: item whose first piece the CTA holds: first row, head, row block | rows << 24, last CTA;
+                          // .w = -1: none, kGaveUp: none, and its own pieces are not all there
     unsigned* err;
 };
 
@@ -623,7 +625,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv4_rows_kernel(con
                 }
         // The producer may set the flag at any time, so the warps leave by what they brought to the barrier, which is the
         // same for all four: one that left while another went on to the next barrier would keep it there for good.
-        if (consumers_meet(!ok || *abort_flag)) break;
+        if (consumers_meet(!ok || *abort_flag)) {
+            join = make_int4(0, 0, 0, kGaveUp);
+            break;
+        }
         const bool starts = begin == it.first, ends = end == it.end;
         const bool whole = starts && ends;
         float* slot = a.slots + (size_t)(2 * c + (starts ? 1 : 0)) * RB * (D + 2);
@@ -695,12 +700,17 @@ __global__ void __launch_bounds__(32 * WARPS) kv4_join_kernel(const RowsArgs a) 
     auto slot = [&](int p) { return a.slots + ((size_t)(2 * (c + p) + (p == 0 ? 1 : 0)) * RB + row) * (D + 2); };
     const int sub = lane / VL, d4 = 4 * (lane % VL);
     float den = 0.0f;
+    bool lost = false;  // a piece is missing: the row is left as it was
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) {
         float m = -INFINITY;
 #pragma unroll 4
-        for (int p = lane; p < pieces; p += 32) m = fmaxf(m, slot(p)[D]);
+        for (int p = lane; p < pieces; p += 32) {
+            m = fmaxf(m, slot(p)[D]);
+            lost |= a.joins[c + p].w == kGaveUp;
+        }
         m = warp_max(m);
+        lost = __any_sync(0xffffffffu, lost);
         constexpr int BATCH = 8 * PP;  // pieces in flight
         for (int p0 = turn * BATCH; p0 < pieces; p0 += share * BATCH) {
             float4 x[8];
@@ -733,7 +743,7 @@ __global__ void __launch_bounds__(32 * WARPS) kv4_join_kernel(const RowsArgs a) 
         }
     }
     if (share > 1) __syncthreads();  // the same for the whole block
-    if (turn || sub || row >= rows) return;
+    if (turn || sub || row >= rows || lost) return;
     for (int w = warp + 1; w < warp + share; ++w) {
         const float4 o = part[w][lane];
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;

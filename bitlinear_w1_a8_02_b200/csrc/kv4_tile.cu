@@ -65,6 +65,7 @@ constexpr int MAX_CTAS = 148;     // sizes the workspace
 constexpr int ITEM_UNITS = 4;
 constexpr int SEQ_GROUP = 32;     // sequences per entry of the coarse unit table
 constexpr uint64_t WAIT_NS = 1000000000ull;
+constexpr int GAVE_UP = -2;
 constexpr float FAR = 16777216.0f;    // scaled maximum whose rounding is one in the exponent
 constexpr float RAISE_SUM = 1024.0f;  // sum of a row's exponentials over a block that raises its maximum
 
@@ -78,7 +79,8 @@ struct TileArgs {
     uint64_t group_inv;  // ceil(2^40 / group): rows / group as a multiplication
     float scale_log2;
     float* slots;   // [2 gridDim.x] pieces: [D / 4][ROWS] float4 sums, then [ROWS] (maximum, denominator)
-    int4* joins;    // [gridDim.x]
+    int4* joins;    // [gridDim.x] item whose first piece the CTA holds: first row, head, item | rows << 20, last CTA;
+                    // .w = -1: none, GAVE_UP: none, and its own pieces are not all there
     unsigned* err;
 };
 
@@ -853,12 +855,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_tile_kernel(const TileArgs a) 
                 *st = make_float2(mx == -INFINITY ? -INFINITY : msc, den == 0.0f && piece_sees ? -0.0f : den);  // -0: as `inv` above
             }
         }
-        if (tid == 0) a.joins[c] = ok ? join : make_int4(0, 0, 0, -1);
+        if (tid == 0) a.joins[c] = join;
     }
 
     // -------------------------------------------------------------------- teardown
     tc::fence_before_sync();
     __syncthreads();
+    if (tid == 0 && abort_sh) a.joins[c] = make_int4(0, 0, 0, GAVE_UP);
     if (warp == MMA_WARP) {
         if (abort_sh) {
             // no MMA may still be using TMEM when it is released
@@ -890,6 +893,7 @@ __global__ void __launch_bounds__(ROWS) kv4_tile_join_kernel(const TileArgs a) {
         const float2 st = reinterpret_cast<const float2*>(slot(p) + ROWS * D)[row];
         m = fmaxf(m, st.x);
         lost |= st.y == 0.0f && signbit(st.y);
+        if (a.joins[c + p].w == GAVE_UP) return;  // a piece is missing: the item is left as it was
     }
     float den = 0.0f;
     float4 v[4];
@@ -940,12 +944,15 @@ __global__ void __launch_bounds__(16 * JOIN_ROWS) kv4_tile_join_few_kernel(const
     auto stat = [&](int p) { return reinterpret_cast<const float2*>(slot(p) + ROWS * D)[row]; };
     float m = -INFINITY;
     int lost = 0;  // a piece saw keys, but scores of -inf only
+    bool gone = false;
 #pragma unroll 4
     for (int p = part; p < pieces; p += 16) {
         const float2 st = stat(p);
         m = fmaxf(m, st.x);
         lost |= st.y == 0.0f && signbit(st.y);
+        gone |= a.joins[c + p].w == GAVE_UP;
     }
+    if (__any_sync(0xffffffffu, gone)) return;  // a piece is missing: the item is left as it was
 #pragma unroll
     for (int o = 2; o < 32; o <<= 1) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -1,5 +1,6 @@
 """What a kernel does before it ends after a wait that gave up, modelled on the CPU: an mbarrier as its phase, waits by
 parity, arrivals that come when they like."""
+import random
 
 
 class Barrier:
@@ -66,3 +67,43 @@ def test_the_stage_that_told_the_end_is_not_waited_for():
         g = 3 * stages + 1
         bars = ring(stages, g, g, True)
         assert not all(bars[s].passes(p) for s, p in drain(g - stages, g, stages))
+
+
+def pieces_of(items, cost, ctas):
+    """The attention's work split: items of `cost` units and their blocks in one line, cut into equal ranges; per CTA the
+    (item, first block, end) that it holds, and per CTA the item that it starts and does not end, with the last CTA of it."""
+    total = sum(cost + n for n in items)
+    ctas = min(ctas, total)
+    held, joins = [], []
+    for c in range(ctas):
+        u0, u1 = total * c // ctas, total * (c + 1) // ctas
+        mine, join, first = [], None, 0
+        for i, n in enumerate(items):
+            b0, b1 = max(0, u0 - first - cost), min(n, u1 - first - cost)
+            if b1 > b0 and u1 > first and u0 < first + cost + n:
+                mine.append((i, b0, b1))
+                if b0 == 0 and b1 < n:
+                    join = (i, ((first + cost + n) * ctas + total - 1) // total - 1)
+            first += cost + n
+        held.append(mine)
+        joins.append(join)
+    return held, joins
+
+
+def test_an_item_with_a_missing_piece_is_not_joined():
+    """A CTA that gave up leaves a mark in place of its own item to join; the joining block of an item looks for marks among
+    the CTAs that hold its pieces. Items without a mark are complete, and what no mark touches is joined."""
+    rng = random.Random(3)
+    for _ in range(300):
+        items = [rng.randint(1, rng.choice([2, 10, 200])) for _ in range(rng.randint(1, 30))]
+        held, joins = pieces_of(items, rng.choice([2, 4]), rng.choice([2, 7, 148, 444]))
+        gone = {c for c in range(len(held)) if rng.random() < 0.2}
+        for c, join in enumerate(joins):
+            if join is None:
+                continue
+            i, last = join
+            blocks = sorted((b0, b1) for d in range(c, last + 1) for j, b0, b1 in held[d] if j == i)
+            assert [b for b, _ in blocks] == [0] + [e for _, e in blocks[:-1]] and blocks[-1][1] == items[i]  # all pieces, in c .. last
+            assert all(any(j == i for j, _, _ in held[d]) for d in range(c, last + 1))
+            complete = not any(d in gone for d in range(len(held)) if any(j == i for j, _, _ in held[d]))
+            assert complete == (c not in gone and not any(d in gone for d in range(c, last + 1)))
