@@ -474,6 +474,10 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // A block's share of its tile's rows, of 2^LS blocks' sums [token][128 rows] in shared memory: a thread keeps four
 // neighbouring rows.
 template <int LS>
@@ -623,7 +627,12 @@ __global__ void __launch_bounds__(FEW_THREADS)
     if (!__all_sync(0xffffffffu, ok)) give_up();
     tc::fence_after_sync();
     int* sums = reinterpret_cast<int*>(ring);
-    if (warp >= 2 && !*aborted) {
+    const bool have = __all_sync(0xffffffffu, ok && !*aborted);
+    if (warp >= 2 && !have) {
+        // no block of the cluster can finish its rows: they all learn of it before they meet
+        if (lane < 1 << f.log_split) st_cluster(tc::map_to_rank(tc::smem_u32(&abort_sh), lane), 1);
+    }
+    if (warp >= 2 && have) {
         const int q = warp & 3;  // the TMEM lane quarter this warp may read
         for (int c = 0; c < f.cols; c += 16) {
             uint32_t v[16];

@@ -19,7 +19,8 @@
 // 2^8 (in the exponent's base-2 units), so accumulators are rarely rescaled. It is
 // taken off the scores before they are scaled: one multiply-add with the scaled
 // maximum would leave that one's rounding, which passes the exponent's range for
-// scores of 2^31 and more.
+// scores of 2^31 and more. (Two instructions a score instead of one, 0.9% of the
+// time; a branch for the rows that need it cost 1.5%.)
 //
 // Work split: all (sequence, head, row block) items are cut into units of 128
 // keys and every CTA takes one contiguous range of units, whatever the lengths

@@ -107,3 +107,19 @@ def test_an_item_with_a_missing_piece_is_not_joined():
             assert all(any(j == i for j, _, _ in held[d]) for d in range(c, last + 1))
             complete = not any(d in gone for d in range(len(held)) if any(j == i for j, _, _ in held[d]))
             assert complete == (c not in gone and not any(d in gone for d in range(c, last + 1)))
+
+
+def test_a_cluster_whose_sums_are_not_all_there_finishes_no_rows():
+    """The blocks of a cluster each hold a part of the sums, written by four warps. A warp that has none to write marks every
+    block before they meet; behind the meeting a block finishes its rows if it has no mark."""
+    rng = random.Random(4)
+    for _ in range(500):
+        blocks = rng.choice([1, 2, 4, 8])
+        have = [[rng.random() < 0.95 for _ in range(4)] for _ in range(blocks)]
+        marked = [False] * blocks
+        for warps in have:
+            for there in warps:
+                if not there:
+                    marked = [True] * blocks
+        for b in range(blocks):
+            assert (not marked[b]) == all(all(w) for w in have)
