@@ -51,7 +51,8 @@ def kv4_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch
                page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor, interleaved: bool = False,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate q and k [M, heads, D] bf16 by their positions' rows of cos_sin [max_pos, D] fp32 (D/2 cosines, D/2 sines),
-    store k and v in the cache and return the rotated q (in `out`, which may be q)."""
+    store k and v in the cache and return the rotated q (in `out`, which may be q). Rows without a sequence or a position are
+    left as they are in `out`."""
     r = _b.native().kv4_append(q, k, v, cos_sin, cache.k_codes, cache.k_steps, cache.v_codes, cache.v_steps, page_table,
                                kv_len, q_start, interleaved, out)
     if type(r) is int:
@@ -60,7 +61,7 @@ def kv4_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch
 
 
 def kv4_read(cache: Kv4Cache, page_table: torch.Tensor, kv_len: torch.Tensor, q_start: torch.Tensor, rows: int):
-    """The cached values of the batch's tokens: (k, v), bf16 [rows, kv_heads, D]."""
+    """The cached values of the batch's tokens: (k, v), bf16 [rows, kv_heads, D]; rows without a token are not set."""
     r = _b.native().kv4_read(cache.k_codes, cache.k_steps, cache.v_codes, cache.v_steps, page_table, kv_len, q_start, rows)
     if type(r) is int:
         _b._check(r, "bitlinear_kv4_read")
@@ -71,7 +72,9 @@ def kv4_attention(q: torch.Tensor, cache: Kv4Cache, page_table: torch.Tensor, kv
                   q_start: torch.Tensor, max_q: int, scale: Optional[float] = None,
                   out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Causal attention of the batch's tokens q [M, Hq, D] bf16 over the cache (their own keys stored before):
-    bf16 [M, Hq, D]. max_q: the largest number of new tokens of a sequence; scale: 1 / sqrt(D) by default."""
+    bf16 [M, Hq, D]. max_q: the largest number of new tokens of a sequence; it chooses the kernel for the whole batch, so a
+    prompt beside single tokens slows these down. scale: 1 / sqrt(D) by default, 2^-100 to 2^100. Rows without a sequence are
+    left as they are in `out`, which must not overlap q."""
     r = _b.native().kv4_attention(q, cache.k_codes, cache.k_steps, cache.v_codes, cache.v_steps, page_table, kv_len,
                                   q_start, max_q, scale, out, ws)
     if type(r) is int:

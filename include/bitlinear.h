@@ -362,8 +362,8 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
  * (paper card "BitNet b1.58 2B4T Technical Report", "Method Adaptation"); the
  * cache format is this library's.
  *
- * Quantisation. A vector (one token, one key/value head, D dims) is cut into
- * groups of 32 consecutive dims. With A = max |x| of a group:
+ * Quantisation. A vector (one token, one key/value head, D dims; keys after their
+ * rotation) is cut into groups of 32 consecutive dims. With A = max |x| of a group:
  *   step = fl(A / 7) rounded to five significant bits (nearest, ties to even);
  *          0 where A < 2^-100
  *   c    = rint(fl(x / step))  in [-7, 7];  0 where step = 0
@@ -393,9 +393,9 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
  * A page may stand in several rows (a shared prefix) where it is only read; the
  * tokens that a call appends must not share a slot.
  * The arrays live on the device, so their contents are checked by the kernels:
- * a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P, a
- * q_start that leaves 0 .. M or decreases, or a position past the rotation table
- * sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
+ * a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P (of a sequence
+ * with new tokens), a q_start that leaves 0 .. M or decreases, or a position past the
+ * rotation table sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
  * access leaves the buffers, and the rows concerned (all rows of a batch whose
  * q_start decreases) are unspecified.
  *
@@ -458,7 +458,9 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  * h / (Hq / Hkv):
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale (q . k_j - max)),  j <= position
  * on the values that the cache holds; products and sums in fp32, p_j rounded to
- * bf16 for the product with v_j. A row that sees no key is zero. A query with a
+ * bf16 for the product with v_j (not in the denominator). The exponentials are good
+ * to 2^-20; where max_q Hq / Hkv > 16, a quarter of them to 7.5e-5. A row that sees
+ * no key is zero. A query with a
  * NaN or an infinity makes its row NaN in that head, and so does a visible key with
  * scale q . k log2(e) above fp32's range; one with q . k above it, and queries of
  * magnitude 2^100 / max(1, scale) or more, may. A key whose score lies below that
@@ -466,7 +468,12 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  *   q, out      [M, Hq, D] device bf16, rows q_stride / out_stride elements apart;
  *               16-byte aligned, strides multiples of 8; must not overlap
  *   max_q       the largest number of new tokens of a sequence (host): a sequence
- *               with more is reported as BL_ERR_BAD_BATCH and left out
+ *               with more is reported as BL_ERR_BAD_BATCH and left out. It chooses the
+ *               kernel for the whole batch: up to max_q Hq / Hkv = 16 one for few rows,
+ *               beyond it one that works on 256 rows at a time, whatever a sequence
+ *               brings. So give it as it is, and send single tokens and prompts in
+ *               calls of their own where time matters (64 tokens on 4096 keys each and
+ *               a prompt of 512: 173 us in one call, 56 and 23 in two)
  *   scale       2^-100 .. 2^100 (commonly 1 / sqrt(D))
  *   ws          bitlinear_workspace_bytes(BL_OP_KV4_ATTENTION, max_q, Hq / Hkv, D) bytes
  * Deterministic: the same inputs give the same bits.
