@@ -319,8 +319,10 @@ bl_status forward_impl(const uint8_t* Wp, const float* gamma, int64_t N, int64_t
     if ((path == Path::GemmTc && !bl::gemm_segments_ok(out, N)) ||
         ((path == Path::GemvFast || path == Path::GemvTc) && !bl::gemv_segments_ok(out, N)))
         path = Path::GemvGeneric;
-    // one kernel (quantise + GEMV) up to 4 tokens where that beats the separate act-quant
-    if (path == Path::GemvFast && bl::gemv_fused_ok(M, K) && bl::gemv_fused_pays(M, N, K))
+    // one kernel (quantise + GEMV) up to 4 tokens where that beats the separate act-quant; not for an output in x's place,
+    // which would be written by some blocks while others still read x
+    const bool in_place = bl::overlap(x, 2 * M * K, out.y, 2 * M * N) || bl::overlap(x, 2 * M * K, out.acc, 4 * M * N);
+    if (path == Path::GemvFast && bl::gemv_fused_ok(M, K) && bl::gemv_fused_pays(M, N, K) && !in_place)
         return cuda_status(bl::launch_gemv(Wp, gamma, N, K, nullptr, nullptr, nullptr, M, out, s, x, rmsnorm));
     BL_TRY(bl::launch_act_quant(x, M, K, layout_of(path), xq, scale, xsum, s, rmsnorm));
     return project(path, Wp, gamma, N, K, xq, scale, xsum, M, out, s, base + w.sk, w.sk_bytes);

@@ -765,12 +765,6 @@ int int8_tile_width(int64_t M, int64_t N, int sms) {
     }
     return width[best];
 }
-
-// Whether n bytes at a and m at b have any in common.
-bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
-}
 }  // namespace
 
 cudaError_t launch_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x, bool rmsnorm,

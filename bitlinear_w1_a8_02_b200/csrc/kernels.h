@@ -151,6 +151,12 @@ cudaError_t launch_ffn_requant_parts(const float* h, const double* part_ss, cons
 cudaError_t launch_ffn_tp_finish(const int32_t* acc, const float* gd, const float* s2, const uint16_t* residual,
                                  uint16_t* y, int64_t M, int64_t d, cudaStream_t s);
 
+// Whether n bytes at a and m at b have any in common.
+inline bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
 // ---- 4-bit paged cache (kv4.cu) and the attention over it (kv4_attn.cu); the
 // structs are in kv4.cuh
 struct Kv4View;

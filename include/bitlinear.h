@@ -25,6 +25,9 @@
  *     bitlinear_get_device_error, which say so.
  *   - No C++ exception crosses this boundary. A failed launch returns BL_ERR_CUDA.
  *   - Calls on different streams may overlap only if their workspaces differ.
+ *   - The output y of a linear layer or FFN may be its x or its residual (an update
+ *     in place; bitlinear_forward_noalloc too). Other arguments must not overlap
+ *     what a call writes, unless the call says so.
  *   - Kernels launch with programmatic dependent launch: a call's kernel may start
  *     while the previous kernel in the stream finishes, and waits for it before
  *     reading its inputs x / h or writing anything. The packed weights (Wp, Wg,
@@ -506,7 +509,7 @@ bl_status bitlinear_pack_weights_int8(const void* W, int wdt, int64_t N, int64_t
  *   Wq        [N, K] device int8, 16-byte aligned; N >= 0, K >= 16, K % 16 == 0
  *   x         [M, K] device bf16, 16-byte aligned; 0 <= M <= 65535
  *   residual  [M, N] device bf16, may be NULL; acc [M, N] device int32, may be NULL
- *   y         [M, N], contiguous; may be x or residual (an update in place)
+ *   y         [M, N], contiguous
  *   ws        bitlinear_workspace_bytes(BL_OP_FORWARD_INT8, M, N, K) bytes
  */
 bl_status bitlinear_forward_int8(const int8_t* Wq, const float* wstep, int64_t N, int64_t K, const uint16_t* x,
