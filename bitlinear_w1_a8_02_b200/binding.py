@@ -131,16 +131,23 @@ def workspace_bytes(op: int, M: int, N: int, K: int) -> int:
 
 
 class Workspace:
-    """A reusable device workspace that grows on demand (one per device)."""
+    """Device workspaces of calls that bring none: one per device and stream, growing on demand, so that calls on different
+    streams share none. A call that is being captured into a graph gets one of its own, which belongs to the graph."""
 
     def __init__(self):
         self._buf = {}
 
     def get(self, device: torch.device, nbytes: int) -> torch.Tensor:
-        buf = self._buf.get(device)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-            self._buf[device] = buf
+        key = (device, torch._C._cuda_getCurrentRawStream(device.index))
+        buf = self._buf.get(key)
+        if buf is None or buf.numel() < nbytes or torch.cuda.is_current_stream_capturing():
+            return self._new(key, nbytes)
+        return buf
+
+    def _new(self, key, nbytes: int) -> torch.Tensor:
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=key[0])
+        if not torch.cuda.is_current_stream_capturing():
+            self._buf[key] = buf
         return buf
 
 
