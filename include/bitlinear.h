@@ -395,10 +395,12 @@ bl_status bitlinear_ffn_tp_finish(const int32_t* acc, const float* gd, const flo
  *               tokens w P .. w P + P - 1. Entries past the last token are not read.
  * A page may stand in several rows (a shared prefix) where it is only read; the
  * tokens that a call appends must not share a slot.
- * The arrays live on the device, so their contents are checked by the kernels:
- * a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P (of a sequence
- * with new tokens), a q_start that leaves 0 .. M or decreases, or a position past the
- * rotation table sets the device error word (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
+ * The arrays live on the device and must not change while a call that was given
+ * them runs (its blocks read them at different times). The kernels check their
+ * contents: a page id outside 0 .. num_pages - 1, a kv_len below 0 or above W P (of
+ * a sequence with new tokens), a q_start that leaves 0 .. M or decreases, or a
+ * position past the rotation table sets the device error word
+ * (bitlinear_get_device_error: BL_ERR_BAD_BATCH); no
  * access leaves the buffers, and the rows concerned (all rows of a batch whose
  * q_start decreases) are unspecified.
  *
@@ -463,11 +465,11 @@ bl_status bitlinear_kv4_read(const bl_kv4_cache* cache, const bl_kv4_batch* batc
  * on the values that the cache holds; products and sums in fp32, p_j rounded to
  * bf16 for the product with v_j (not in the denominator). The exponentials are good
  * to 2^-20; where max_q Hq / Hkv > 16, a quarter of them to 7.5e-5. A row that sees
- * no key is zero. A query with a
- * NaN or an infinity makes its row NaN in that head, and so does a visible key with
- * scale q . k log2(e) above fp32's range; one with q . k above it, and queries of
- * magnitude 2^100 / max(1, scale) or more, may. A key whose score lies below that
- * range weighs nothing beside others. (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
+ * no key is zero. A query with a NaN or an infinity makes its row NaN in that head,
+ * and so does a visible key with scale q . k log2(e) above fp32's range; one with
+ * q . k above it, and queries of magnitude 2^100 / max(1, scale) or more, may. A key
+ * whose score lies below that range weighs nothing beside others.
+ * (M Hq / 256 + S Hkv) (W P / 128 + 8) < 2^31.
  *   q, out      [M, Hq, D] device bf16, rows q_stride / out_stride elements apart;
  *               16-byte aligned, strides multiples of 8; must not overlap
  *   max_q       the largest number of new tokens of a sequence (host): a sequence
